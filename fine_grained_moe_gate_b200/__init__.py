@@ -39,6 +39,8 @@ EXPORTS = (
     "moe_layer_forward_fp8",
     "moe_ep_plan_size", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_return",
     "moe_layer_backward", "moe_backward_workspace_size",
+    "moe_gate_logits", "moe_route_logits", "moe_route_logits_backward", "moe_ffn_up_save",
+    "moe_swiglu_backward_saved",
 )
 
 MOE_ROUTED, MOE_SHARED = 0, 1
@@ -82,6 +84,34 @@ def fp8_experts(q: dict) -> MoEFp8Experts:
     return MoEFp8Experts(**f)
 
 
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+
+
+class MoERouteOpts(ctypes.Structure):
+    """moe_route_opts: the form of the gate (see moe_gate.h)."""
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def route_opts(score="sigmoid", groups=1, top_groups=1, group_top=1, renormalize=True, scale=1.0) -> MoERouteOpts:
+    """MoERouteOpts from plain values; the defaults are moe_route's own gate."""
+    kinds = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
+    if score not in kinds:
+        raise ValueError(f"score must be one of {sorted(kinds)}, got {score!r}")
+    return MoERouteOpts(kinds[score], groups, top_groups, group_top, int(bool(renormalize)), scale)
+
+
+class MoESavedActs(ctypes.Structure):
+    """moe_saved_acts: the gate/up pre-activations of a forward in 8 bits."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("a", "a_scale", "g", "g_scale", "sa", "sa_scale", "sg", "sg_scale")]
+
+
+def saved_acts(t: dict) -> MoESavedActs:
+    """MoESavedActs from a dict of device tensors under its field names (the
+    layout of ``saved_act_buffers``).  The tensors must outlive its use."""
+    return MoESavedActs(*[_p(t.get(n)) for n, _ in MoESavedActs._fields_])
+
+
 _lib = None
 
 
@@ -120,6 +150,11 @@ def lib() -> ctypes.CDLL:
             "moe_ep_dispatch": [P, P, P, ctypes.c_int32, ctypes.c_int32, S, P, P],
             "moe_ep_return": [P, P, ctypes.c_int32, ctypes.c_int32, S, P, P],
             "moe_selftest_bounded_wait": [ctypes.c_uint32, P],
+            "moe_gate_logits": [P, P, S, P, P],
+            "moe_route_logits": [P, P, S, MoERouteOpts, P, P, P, P],
+            "moe_route_logits_backward": [P, P, P, P, S, MoERouteOpts, P, P],
+            "moe_ffn_up_save": [P, P, P, P, P, P, P, S, P, P, ctypes.POINTER(MoESavedActs), P],
+            "moe_swiglu_backward_saved": [ctypes.POINTER(MoESavedActs), S, ctypes.c_int32, P, P, P, P, P, P, P],
             "moe_layer_backward": [P, P, P, P, P, P, P, P, S, P, P, P, P, P, F, ctypes.c_int32, P, P, P, P, P, P, P,
                                    P, P, P, sz, P],
         }
@@ -394,6 +429,49 @@ def quantize_experts_fp8(p: dict, stream=None) -> dict:
         moe_quantize_fp8(w, d, Is, S, MOE_SF_WEIGHTS, q, sc, stream)
         out["ws2q"], out["ws2s"] = q, sc
     return out
+
+
+# ---- routing from logits -----------------------------------------------------
+
+def moe_gate_logits(x, w_gate, shape, logits, stream=None):
+    _check(lib().moe_gate_logits(_p(x), _p(w_gate), shape, _p(logits), _stream(stream)), "moe_gate_logits")
+
+
+def moe_route_logits(logits, bias, shape, opts, topk_idx, topk_w, counts, stream=None):
+    _check(lib().moe_route_logits(_p(logits), _p(bias), shape, opts, _p(topk_idx), _p(topk_w), _p(counts),
+                                  _stream(stream)), "moe_route_logits")
+
+
+def moe_route_logits_backward(logits, topk_idx, dw, dscores, shape, opts, dlogits, stream=None):
+    _check(lib().moe_route_logits_backward(_p(logits), _p(topk_idx), _p(dw), _p(dscores), shape, opts, _p(dlogits),
+                                           _stream(stream)), "moe_route_logits_backward")
+
+
+# ---- activations saved in 8 bits -----------------------------------------------
+
+def saved_act_buffers(shape, device) -> dict:
+    """Uninitialised device buffers for the saved pre-activations of a layer
+    (uint8 tensors under MoESavedActs' field names; the shared ones only with
+    shape.S > 0): pass saved_acts(...) of them to the calls."""
+    import torch
+    out = {}
+    sets = [("", shape.T * shape.k, shape.I)] + ([("s", shape.T, shape.S * shape.Is)] if shape.S > 0 else [])
+    for pre, rows, n in sets:
+        for name in ("a", "g"):
+            out[pre + name] = torch.empty((rows, n), dtype=torch.uint8, device=device)
+            out[pre + name + "_scale"] = torch.empty(moe_fp8_scale_bytes(rows, n, MOE_SF_TOKENS), dtype=torch.uint8,
+                                                     device=device)
+    return out
+
+
+def moe_ffn_up_save(x_perm, offsets, w1, w3, x, ws1, ws3, shape, h, hs, saved, stream=None):
+    _check(lib().moe_ffn_up_save(_p(x_perm), _p(offsets), _p(w1), _p(w3), _p(x), _p(ws1), _p(ws3), shape, _p(h),
+                                 _p(hs), ctypes.byref(saved), _stream(stream)), "moe_ffn_up_save")
+
+
+def moe_swiglu_backward_saved(saved, shape, expert_set, u, perm_tok, topk_w, dadg, h, dw, stream=None):
+    _check(lib().moe_swiglu_backward_saved(ctypes.byref(saved), shape, expert_set, _p(u), _p(perm_tok), _p(topk_w),
+                                           _p(dadg), _p(h), _p(dw), _stream(stream)), "moe_swiglu_backward_saved")
 
 
 # ---- expert parallelism --------------------------------------------------------

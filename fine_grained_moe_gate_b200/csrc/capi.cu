@@ -229,6 +229,74 @@ moe_status do_swiglu(const void* x_perm, const int32_t* offsets, const void* w1,
     return do_ffn_down(h, offsets, w2, shared ? hs : nullptr, ws2, sh, y_perm, shared_out, status, sms, st);
 }
 
+// ---- routing from logits, saved activations ----------------------------------
+
+constexpr int kMaxRouteGroups = 32;
+
+moe_status validate_opts(const moe_route_opts& o, const moe_shape& sh) {
+    if (o.score != MOE_SCORE_SIGMOID && o.score != MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID_ARG;
+    if (o.groups <= 0 || sh.E % o.groups != 0) return MOE_ERR_INVALID_ARG;
+    if (o.top_groups <= 0 || o.top_groups > o.groups) return MOE_ERR_INVALID_ARG;
+    if (o.group_top != 1 && o.group_top != 2) return MOE_ERR_INVALID_ARG;
+    if (o.renormalize != 0 && o.renormalize != 1) return MOE_ERR_INVALID_ARG;
+    if ((long long)o.top_groups * (sh.E / o.groups) < sh.k) return MOE_ERR_INVALID_ARG;
+    if (!(o.scale - o.scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // NaN or infinite
+    return o.groups > kMaxRouteGroups ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe::RouteOpts route_opts(const moe_route_opts& o) {
+    return moe::RouteOpts{o.score == MOE_SCORE_SOFTMAX, o.groups, o.top_groups, o.group_top, o.renormalize, o.scale};
+}
+
+moe_status do_gate_logits(const void* x, const void* w_gate, const moe_shape& sh, float* logits, int* status, int sms,
+                          cudaStream_t st) {
+    const cudaError_t err =
+        sh.dtype != MOE_F32  // x and W_gate are bf16 for MOE_FP8_E4M3 too
+            ? moe::launch_gate_logits_tc(x, w_gate, sh.T, sh.d, sh.E, logits, status, sms, st)
+            : moe::launch_gate_logits_simt(static_cast<const float*>(x), static_cast<const float*>(w_gate), sh.T, sh.d,
+                                           sh.E, logits, st);
+    return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool saved_ok(const moe_saved_acts& s, bool shared) {
+    return shared ? s.sa && s.sa_scale && s.sg && s.sg_scale : s.a && s.a_scale && s.g && s.g_scale;
+}
+bool saved_aligned(const moe_saved_acts& s) {
+    return aligned16(s.a) && aligned16(s.a_scale) && aligned16(s.g) && aligned16(s.g_scale) && aligned16(s.sa) &&
+           aligned16(s.sa_scale) && aligned16(s.sg) && aligned16(s.sg_scale);
+}
+
+void tc_up_save(moe::TcUpArgs& u, uint8_t* a, void* as, uint8_t* g, void* gs) {
+    u.save_a = a;
+    u.save_as = static_cast<uint8_t*>(as);
+    u.save_g = g;
+    u.save_gs = static_cast<uint8_t*>(gs);
+}
+
+moe_status do_ffn_up_save(const void* x_perm, const int32_t* offsets, const void* w1, const void* w3, const void* x,
+                          const void* ws1, const void* ws3, const moe_shape& sh, void* h, void* hs,
+                          const moe_saved_acts& s, int* status, int sms, cudaStream_t st) {
+    if (sh.T == 0) return MOE_OK;
+    const bool shared = x && sh.S > 0;
+    moe::TcUpArgs ur = tc_up_args(x_perm, nullptr, offsets, w1, w3, sh, false, h);
+    tc_up_save(ur, s.a, s.a_scale, s.g, s.g_scale);
+    moe::TcUpArgs us = tc_up_args(x, nullptr, nullptr, ws1, ws3, sh, true, hs);
+    tc_up_save(us, s.sa, s.sa_scale, s.sg, s.sg_scale);
+    return moe::launch_tc_up(&ur, shared ? &us : nullptr, status, sms, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// the saved codes of one expert set
+moe::SwigluBwdSaved saved_bwd_args(const moe_saved_acts& s, const moe_shape& sh, bool shared) {
+    moe::SwigluBwdSaved p{};
+    p.a = shared ? s.sa : s.a;
+    p.a_scale = static_cast<const uint8_t*>(shared ? s.sa_scale : s.a_scale);
+    p.g = shared ? s.sg : s.g;
+    p.g_scale = static_cast<const uint8_t*>(shared ? s.sg_scale : s.g_scale);
+    p.rows = shared ? sh.T : (long long)sh.T * sh.k;
+    p.n = shared ? sh.S * sh.Is : sh.I;
+    return p;
+}
+
 // ---- FP8 experts -----------------------------------------------------------
 
 
@@ -726,6 +794,112 @@ moe_status moe_layer_forward(const void* x, const void* w_gate, const float* bia
                                st) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+// ---- routing from logits -----------------------------------------------------
+
+moe_status moe_gate_logits(const void* x, const void* w_gate, moe_shape sh, float* logits, void* stream) {
+    moe_status v = validate_shape(sh);
+    if (v != MOE_OK) return v;
+    MOE_REQUIRE(w_gate, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || (x && logits), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(x) && aligned16(w_gate) && aligned16(logits), MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    return do_gate_logits(x, w_gate, sh, logits, status, sms, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_route_logits(const float* logits, const float* bias, moe_shape sh, moe_route_opts opts,
+                            int32_t* topk_idx, float* topk_w, int32_t* counts, void* stream) {
+    moe_status v = validate_shape(sh);
+    if (v == MOE_OK) v = validate_opts(opts, sh);
+    if (v != MOE_OK) return v;
+    MOE_REQUIRE(counts, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || (logits && topk_idx && topk_w), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(logits) && aligned16(bias) && aligned16(topk_idx) && aligned16(topk_w) && aligned16(counts),
+                MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    return moe::launch_route_logits(logits, bias, sh.T, sh.E, sh.k, route_opts(opts), topk_idx, topk_w, counts, status,
+                                    sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+moe_status moe_route_logits_backward(const float* logits, const int32_t* topk_idx, const float* dw,
+                                     const float* dscores, moe_shape sh, moe_route_opts opts, float* dlogits,
+                                     void* stream) {
+    moe_status v = validate_shape(sh);
+    if (v == MOE_OK) v = validate_opts(opts, sh);
+    if (v != MOE_OK) return v;
+    MOE_REQUIRE(sh.T == 0 || (logits && topk_idx && dw && dlogits), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(logits) && aligned16(topk_idx) && aligned16(dw) && aligned16(dscores) && aligned16(dlogits),
+                MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    return moe::launch_route_logits_bwd(logits, topk_idx, dw, dscores, sh.T, sh.E, sh.k, route_opts(opts), dlogits,
+                                        status, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+// ---- activations saved in 8 bits ----------------------------------------------
+
+moe_status moe_ffn_up_save(const void* x_perm, const int32_t* offsets, const void* w1, const void* w3, const void* x,
+                           const void* ws1, const void* ws3, moe_shape sh, void* h, void* hs,
+                           const moe_saved_acts* saved, void* stream) {
+    moe_status v = validate_dense_weights(sh);
+    if (v != MOE_OK) return v;
+    MOE_REQUIRE(sh.dtype == MOE_BF16, MOE_ERR_UNSUPPORTED);
+    const bool shared = x != nullptr && sh.S > 0;
+    MOE_REQUIRE(offsets && w1 && w3 && saved, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || (x_perm && h && saved_ok(*saved, false)), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(!shared || (ws1 && ws3 && (sh.T == 0 || (hs && saved_ok(*saved, true)))), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(x_perm) && aligned16(offsets) && aligned16(w1) && aligned16(w3) && aligned16(x) &&
+                    aligned16(ws1) && aligned16(ws3) && aligned16(h) && aligned16(hs) && saved_aligned(*saved),
+                MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    return do_ffn_up_save(x_perm, offsets, w1, w3, shared ? x : nullptr, ws1, ws3, sh, h, hs, *saved, status, sms,
+                          static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_swiglu_backward_saved(const moe_saved_acts* saved, moe_shape sh, int32_t set, const float* u,
+                                     const int32_t* perm_tok, const float* topk_w, void* dadg, void* h, float* dw,
+                                     void* stream) {
+    moe_status v = validate_dense_weights(sh);
+    if (v != MOE_OK) return v;
+    MOE_REQUIRE(sh.dtype == MOE_BF16, MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(set == MOE_ROUTED || (set == MOE_SHARED && sh.S > 0), MOE_ERR_INVALID_ARG);
+    const bool shared = set == MOE_SHARED;
+    MOE_REQUIRE(saved, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || (saved_ok(*saved, shared) && u && dadg), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || shared || (perm_tok && topk_w && dw), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(saved_aligned(*saved) && aligned16(u) && aligned16(perm_tok) && aligned16(topk_w) && aligned16(dadg) &&
+                    aligned16(h) && aligned16(dw),
+                MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    moe::SwigluBwdSaved p = saved_bwd_args(*saved, sh, shared);
+    p.u = u;
+    p.perm = shared ? nullptr : perm_tok;
+    p.w = topk_w;
+    p.dadg = static_cast<uint16_t*>(dadg);
+    p.h = static_cast<uint16_t*>(h);
+    p.dw = dw;
+    p.status = status;
+    return moe::launch_swiglu_bwd_saved(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+                                                                                                  : MOE_ERR_CUDA;
 }
 
 size_t moe_fp8_scale_bytes(int64_t rows, int32_t K, int32_t layout) {

@@ -236,6 +236,12 @@ struct SetParams {
     // up rows into g_out, [rows][ldo]) beside h.
     float* a_out;
     float* g_out;
+    // up, bf16 with SAVE: a and g as E4M3 codes [rows][ldo] and their scale
+    // words [ldo / 128][a_rows] beside h.
+    uint8_t* save_a;
+    uint8_t* save_as;
+    uint8_t* save_g;
+    uint8_t* save_gs;
 };
 struct Params {
     const int32_t* offsets;
@@ -418,7 +424,24 @@ __device__ __forceinline__ int next_acc(int prev, int n_mma) {
     return (F8 && a == 1 && n_mma > (int)ACC1_COLS_F8) ? 0 : a;
 }
 
-template <bool UP, bool F8>
+// Eight consecutive features of a token as E4M3: the four lanes of its 32
+// features share the tile's exponent, taken from the fp32 values.  Returns
+// the tile's scale byte; every lane of the warp calls it.
+__device__ __forceinline__ uint32_t quantize_tile8(const float4& x, const float4& y, bool ok, uint2& codes) {
+    float amax = fmaxf(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))),
+                       fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+    if (!ok) amax = 0.0f;
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int ex = mx_tile_exponent(amax);
+    const float mul = mx_inv_scale(ex);
+    codes.x = e4m3x2(__fmul_rn(x.x, mul), __fmul_rn(x.y, mul)) | (e4m3x2(__fmul_rn(x.z, mul), __fmul_rn(x.w, mul)) << 16);
+    codes.y = e4m3x2(__fmul_rn(y.x, mul), __fmul_rn(y.y, mul)) | (e4m3x2(__fmul_rn(y.z, mul), __fmul_rn(y.w, mul)) << 16);
+    return (uint32_t)(ex + 127);
+}
+
+// SAVE (bf16 up only): the pre-activations leave in 8 bits beside h.
+template <bool UP, bool F8, bool SAVE = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(n_threads<UP, F8>(), 1)
     tc_grouped_gemm_kernel(const __grid_constant__ SetMaps ma, const __grid_constant__ SetMaps mb,
                            const __grid_constant__ CUtensorMap tmXg, const Params p) {
@@ -859,6 +882,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(n_threads<UP, F8>(),
                     float4 u0 = *reinterpret_cast<const float4*>(row + 64 + fj);
                     float4 u1 = *reinterpret_cast<const float4*>(row + 64 + fj + 4);
                     if (NXB == 1) named_bar_sync(1 + eg, 128);  // the single buffer is free for the next chunk
+                    if (SAVE) {
+                        uint2 ca, cg;
+                        const uint32_t ba = quantize_tile8(g0, g1, tok_ok, ca), bg = quantize_tile8(u0, u1, tok_ok, cg);
+                        const uint32_t ba2 = __shfl_xor_sync(0xffffffffu, ba, 4), bg2 = __shfl_xor_sync(0xffffffffu, bg, 4);
+                        if (tok_ok) {
+                            const size_t row_ = (size_t)(tok0 + c + my_tok);
+                            const size_t o = row_ * sp.ldo + fcta + fj;
+                            *reinterpret_cast<uint2*>(sp.save_a + o) = ca;
+                            *reinterpret_cast<uint2*>(sp.save_g + o) = cg;
+                            if (part == 0) {  // this CTA's two tiles: half of the row's word of the stage
+                                const size_t so =
+                                    ((size_t)(fcta >> 7) * (size_t)sp.a_rows + row_) * 4 + ((fcta & 127) >> 5);
+                                *reinterpret_cast<uint16_t*>(sp.save_as + so) = (uint16_t)(ba | (ba2 << 8));
+                                *reinterpret_cast<uint16_t*>(sp.save_gs + so) = (uint16_t)(bg | (bg2 << 8));
+                            }
+                        }
+                    }
                     if (F8 && sp.q_out) {
                         // h rounded to bf16 (as the plain output), then its 1x32 tiles to E4M3: the four lanes
                         // of a token's 32 features share the tile's largest magnitude
@@ -970,9 +1010,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(n_threads<UP, F8>(),
 
 std::atomic<unsigned int> g_sched_seq{0};
 
-template <bool UP, bool F8>
+template <bool UP, bool F8, bool SAVE = false>
 cudaError_t launch(const SetMaps& a, const SetMaps& b, const CUtensorMap& xg, Params p, int num_sms, cudaStream_t st) {
-    auto kern = tc_grouped_gemm_kernel<UP, F8>;
+    auto kern = tc_grouped_gemm_kernel<UP, F8, SAVE>;
     p.sched_slot = (int)(g_sched_seq.fetch_add(1u, std::memory_order_relaxed) % (unsigned int)kSchedSlots);
     constexpr size_t SMEM = smem_bytes<UP, F8>();
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
@@ -1016,6 +1056,11 @@ bool up_set(const TcUpArgs& a, SetMaps& m, SetParams& sp) {
     sp.a_out = a.f8 ? nullptr : a.pre_a;
     sp.g_out = a.f8 ? nullptr : a.pre_g;
     if (!sp.a_out != !sp.g_out) return false;
+    sp.save_a = a.save_a;
+    sp.save_as = a.save_as;
+    sp.save_g = a.save_g;
+    sp.save_gs = a.save_gs;
+    if (a.save_a && (a.f8 || a.gather || !a.save_as || !a.save_g || !a.save_gs)) return false;
     return true;
 }
 
@@ -1083,6 +1128,9 @@ cudaError_t launch_tc_up(const TcUpArgs* routed, const TcUpArgs* shared, int* st
     if (!shared) mb = ma;
     p.status = status;
     const bool f8 = routed ? routed->f8 : shared->f8;
+    const bool save = (routed ? routed->save_a : shared->save_a) != nullptr;
+    if (routed && shared && save != (shared->save_a != nullptr)) return cudaErrorInvalidValue;
+    if (save) return launch<true, false, true>(ma, mb, xg, p, num_sms, st);
     return f8 ? launch<true, true>(ma, mb, xg, p, num_sms, st) : launch<true, false>(ma, mb, xg, p, num_sms, st);
 }
 

@@ -71,6 +71,42 @@ cudaError_t launch_router_tc(const void* x, const void* wg, const float* bias, i
                              int32_t* idx, float* w, int32_t* counts, float* aff, int* status, int num_sms,
                              cudaStream_t st);
 
+// Gate logits z = x W_g^T, fp32 [T][E]: router_tc.cu (bf16, tensor cores), router.cu (fp32)
+cudaError_t launch_gate_logits_tc(const void* x, const void* wg, int T, int d, int E, float* logits, int* status,
+                                  int num_sms, cudaStream_t st);
+cudaError_t launch_gate_logits_simt(const float* x, const float* wg, int T, int d, int E, float* logits,
+                                    cudaStream_t st);
+
+// route_logits.cu: routing from logits and its gradient (fields as moe_route_opts, validated)
+struct RouteOpts {
+    int softmax, groups, top_groups, group_top, renormalize;
+    float scale;
+};
+cudaError_t launch_route_logits(const float* logits, const float* bias, int T, int E, int k, const RouteOpts& o,
+                                int32_t* idx, float* w, int32_t* counts, int* status, int num_sms, cudaStream_t st);
+cudaError_t launch_route_logits_bwd(const float* logits, const int32_t* idx, const float* dw, const float* dscores,
+                                    int T, int E, int k, const RouteOpts& o, float* dlogits, int* status, int num_sms,
+                                    cudaStream_t st);
+
+// act_save.cu: the SwiGLU backward from saved 8-bit pre-activations.  Codes
+// [rows][n] with token-layout scale words [n / 128][rows]; u, dadg ([..][2n])
+// and h (may be null) hold row r at prow[r] (prow null: r).  perm null: the
+// shared set (weight 1, no dw).
+struct SwigluBwdSaved {
+    const uint8_t *a, *a_scale, *g, *g_scale;
+    const float* u;
+    const int32_t* prow;
+    const int32_t* perm;
+    const float* w;
+    uint16_t* dadg;
+    uint16_t* h;
+    float* dw;
+    long long rows;
+    int n;
+    int* status;
+};
+cudaError_t launch_swiglu_bwd_saved(const SwigluBwdSaved& p, int num_sms, cudaStream_t st);
+
 // permute.cu
 size_t permute_scratch_bytes(int T, int E);
 cudaError_t launch_permute(const void* x, const int32_t* idx, const int32_t* counts, int T, int d, int E, int k,
@@ -178,6 +214,13 @@ struct TcUpArgs {
     // backward's recompute).
     float* pre_a = nullptr;
     float* pre_g = nullptr;
+    // bf16 only, optional: also save a and g as E4M3 codes [A_rows][I] with
+    // token-layout scale words [I / 128][A_rows] (quant.cu's rule, from the
+    // fp32 sums).  All four or none; both sets of a launch alike.
+    uint8_t* save_a = nullptr;
+    uint8_t* save_as = nullptr;
+    uint8_t* save_g = nullptr;
+    uint8_t* save_gs = nullptr;
 };
 // Down projection: Y[r][:] = H[r] . W2_g^T, W2_g = [d][K] (K = I), or for
 // the shared group S stacked [d][Is] blocks contracted over K = S * Is.

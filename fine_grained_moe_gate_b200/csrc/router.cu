@@ -134,6 +134,58 @@ cudaError_t launch_router_simt(const void* x, const void* wg, const float* bias,
 }
 
 // ---------------------------------------------------------------------------
+// Gate logits of an fp32 layer: z = x W_gate^T, FFMA in k order.  A CTA takes
+// 32 tokens x 32 experts (small layers: many small tiles fill more SMs than
+// the router's 32 tokens x E), each of its 128 threads 2 x 4 of them; 32-wide
+// K chunks go through shared memory.
+__global__ void __launch_bounds__(128) gate_logits_simt_kernel(const float* __restrict__ x,
+                                                               const float* __restrict__ wg, int T, int d, int E,
+                                                               float* __restrict__ z) {
+    constexpr int KC = 32;
+    __shared__ float xs[KC][33], ws[KC][36];
+    const int tid = threadIdx.x, t0 = blockIdx.x * 32, e0 = blockIdx.y * 32;
+    const int tr = tid >> 3, ec = (tid & 7) * 4;  // tokens tr, tr + 16; experts ec .. ec + 3
+    float acc[2][4] = {};
+    for (int c0 = 0; c0 < d; c0 += KC) {
+        __syncthreads();
+        for (int i = tid; i < 32 * KC; i += 128) {
+            const int r = i >> 5, c = i & 31;
+            const bool in = c0 + c < d;
+            xs[c][r] = in && t0 + r < T ? x[(size_t)(t0 + r) * d + c0 + c] : 0.0f;
+            ws[c][r] = in && e0 + r < E ? wg[(size_t)(e0 + r) * d + c0 + c] : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            const float a0 = xs[c][tr], a1 = xs[c][tr + 16];
+            const float4 b = *reinterpret_cast<const float4*>(&ws[c][ec]);
+            const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[0][i] = fmaf(a0, bv[i], acc[0][i]);
+                acc[1][i] = fmaf(a1, bv[i], acc[1][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + tr + 16 * h, e = e0 + ec + i;
+            if (t < T && e < E) z[(size_t)t * E + e] = acc[h][i];
+        }
+}
+
+cudaError_t launch_gate_logits_simt(const float* x, const float* wg, int T, int d, int E, float* logits,
+                                    cudaStream_t st) {
+    if (T == 0) return cudaSuccess;
+    const dim3 grid((unsigned)((T + 31) / 32), (unsigned)((E + 31) / 32));
+    gate_logits_simt_kernel<<<grid, 128, 0, st>>>(x, wg, T, d, E, logits);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
 // Bias update: one thread per expert, every operation a single IEEE fp32
 // rounding (no contraction), so the result is a deterministic function of
 // (counts, bias).

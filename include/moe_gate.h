@@ -444,6 +444,105 @@ MOE_API moe_status moe_layer_forward_fp8(const void* x, const void* w_gate, cons
                                          void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Routing from gate logits  [P1 "In code", route(): scores, biased choice,
+ * weights from the unbiased scores; P2 DeepSeekMoE sketch: softmax gating].
+ * moe_route is the layer's own gate (sigmoid, one group, renormalised) fused
+ * with the gate product; these calls keep the product, the choice and its
+ * gradient apart and cover the other forms of the family:
+ *   score       MOE_SCORE_SIGMOID s_i = 1 / (1 + e^-z_i)
+ *               MOE_SCORE_SOFTMAX s_i = e^z_i / sum_j e^z_j over all E
+ *   groups      the E experts form `groups` runs of E / groups consecutive
+ *               experts (groups must divide E, at most 32)
+ *   top_groups  experts are chosen from that many groups only, those with the
+ *               largest group value: the sum of the group's `group_top` (1 or
+ *               2) largest choice values; top_groups * E / groups >= k.
+ *               top_groups == groups: no restriction (the values are not used)
+ *   renormalize 1: weights divided by the sum over the chosen k;  0: as scored
+ *   scale       finite factor on the weights
+ * -------------------------------------------------------------------------*/
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+typedef struct {
+    int32_t score, groups, top_groups, group_top, renormalize;
+    float scale;
+} moe_route_opts;
+
+/* moe_gate_logits -- z[t][i] = x[t] . W_gate[i], fp32 accumulate and output
+ * (for bf16 x and W_gate the product moe_route takes its scores from).
+ * x [T][d], W_gate [E][d] dtype (bf16 for MOE_FP8_E4M3 too); logits [T][E]. */
+MOE_API moe_status moe_gate_logits(const void* x, const void* w_gate, moe_shape sh, float* logits, void* stream);
+
+/* moe_route_logits -- the choice:
+ *   v[t][i]  = s[t][i] + bias[i]  (bias NULL: v = s), taken in 64 bits
+ *   topk_idx[t][0..k) the k largest v of the kept groups, descending; equal v
+ *            -> lower index; equal group values -> lower group
+ *   topk_w[t][j] = scale * s[idx_j]  ( / sum_j' s[idx_j'] )
+ *   counts[i]    as moe_route (overwritten)
+ * The order is that of the 64-bit values: v closer to each other than the
+ * error of their 32-bit form is evaluated again in 64 bits.
+ * An expert with logit -inf, or with v -inf (bias -inf), is masked: it has no
+ * score, is never chosen and counts in no group value.  A NaN logit is masked
+ * too and reported (MOE_ERR_DEVICE_CHECK via moe_get_last_error).  A token
+ * with fewer than k experts to choose from gets index -1 and weight 0 in the
+ * slots left, and is reported likewise.  logit +inf: the limit of the formula.
+ * logits [T][E] fp32; of sh only T, E and k matter here (the rest has to be
+ * valid).  Results do not depend on T or on a token's place. */
+MOE_API moe_status moe_route_logits(const float* logits, const float* bias, moe_shape sh, moe_route_opts opts,
+                                    int32_t* topk_idx, float* topk_w, int32_t* counts, void* stream);
+
+/* moe_route_logits_backward -- the gradient of the logits for the choice made
+ * (the choice, the groups and the bias carry none):
+ *   dlogits = d/dz ( <dw, topk_w> + <dscores, s> )        [T][E], overwritten
+ * dw [T][k]; dscores NULL or [T][E] (a loss on the scores, e.g. for balance).
+ * Slots with index -1 are skipped; another index outside [0, E) is skipped
+ * and reported (MOE_ERR_DEVICE_CHECK).  Masked experts (logit -inf or NaN)
+ * get 0, whatever dscores holds there.  An expert listed twice gets the sum. */
+MOE_API moe_status moe_route_logits_backward(const float* logits, const int32_t* topk_idx, const float* dw,
+                                             const float* dscores, moe_shape sh, moe_route_opts opts, float* dlogits,
+                                             void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Activations saved in 8 bits  [P1 "The idea": FP8 with fine-grained
+ * quantization tiles].  The layer backward needs the gate/up pre-activations
+ * a = x W1^T and g = x W3^T.  moe_layer_backward runs that product again;
+ * with the calls below the forward keeps a and g as E4M3 codes with a
+ * power-of-two scale per tile of 32 features (moe_quantize_fp8's rule, taken
+ * from the fp32 sums) and the backward reads them: 2 * (1 + 1/32) bytes per
+ * row and feature instead of a third of the backward's products.
+ * Codes have the rows of h; the scales of an [rows][n] matrix are the
+ * MOE_SF_TOKENS words [n / 128][rows], moe_fp8_scale_bytes(rows, n,
+ * MOE_SF_TOKENS) bytes.  Routed: rows T*k in moe_permute's order, n = I;
+ * shared: rows T, n = S * Is (NULL when S == 0).  Device pointers, 16-byte
+ * aligned.  MOE_BF16 layers only (MOE_ERR_UNSUPPORTED otherwise).
+ * -------------------------------------------------------------------------*/
+typedef struct {
+    uint8_t* a;  void* a_scale;     /* routed gate pre-activations  */
+    uint8_t* g;  void* g_scale;     /* routed up pre-activations    */
+    uint8_t* sa; void* sa_scale;    /* shared                       */
+    uint8_t* sg; void* sg_scale;
+} moe_saved_acts;
+
+/* moe_ffn_up_save -- moe_ffn_up, and a and g of every row into `saved` from
+ * the same launch's accumulators.  h and hs are bit-identical to
+ * moe_ffn_up's.  x == NULL or S == 0 leaves the shared set out. */
+MOE_API moe_status moe_ffn_up_save(const void* x_perm, const int32_t* offsets, const void* w1, const void* w3,
+                                   const void* x, const void* ws1, const void* ws3, moe_shape sh, void* h, void* hs,
+                                   const moe_saved_acts* saved, void* stream);
+
+/* moe_swiglu_backward_saved -- the SwiGLU backward of one expert set from the
+ * saved a and g (as the values their codes stand for), s = sigmoid(a):
+ *   dh = wt * u,  dadg[r] = [ dh g s (1 + a (1 - s)) | dh a s ]   [rows][2n]
+ *   h[r] = a s g                                  [rows][n], NULL: not wanted
+ * MOE_ROUTED: row r is assignment q = perm_tok[r], wt = topk_w[q], and dw[q]
+ *   = sum_i u[r][i] (a s g)[i] (unrounded), the gradient of topk_w for u = dy
+ *   W2;  perm_tok [T*k], topk_w [T*k], dw [T*k].  An entry of perm_tok outside
+ *   [0, T*k) is reported (MOE_ERR_DEVICE_CHECK); its row gets zeros.
+ * MOE_SHARED: wt = 1; perm_tok, topk_w and dw are ignored (may be NULL).
+ * u [rows][n] fp32 (the gradient at h before the weight); dadg, h bf16. */
+MOE_API moe_status moe_swiglu_backward_saved(const moe_saved_acts* saved, moe_shape sh, int32_t set, const float* u,
+                                             const int32_t* perm_tok, const float* topk_w, void* dadg, void* h,
+                                             float* dw, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Expert parallelism (no counterpart in the pages' code; their "custom
  * all-to-all kernels for MoE dispatch/combine", crackai.dev "DeepSeek-V3",
  * "How It Works").  W ranks, one per GPU; rank o owns experts

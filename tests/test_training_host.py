@@ -1,0 +1,155 @@
+"""Host-side checks of the routing-from-logits and saved-activation calls: every
+refusal comes back before anything reaches a device."""
+import ctypes
+import os
+
+import pytest
+
+import fine_grained_moe_gate_b200 as moe
+
+INVALID, UNSUPPORTED, ALIGN, WORKSPACE = 1, 2, 3, 4
+FAKE = 1 << 20  # a 16-byte aligned non-null "pointer" never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(moe.LIB_PATH):
+        from fine_grained_moe_gate_b200 import build
+        build.build()
+    return moe.lib()
+
+
+def shape(**kw):
+    base = dict(T=128, d=256, E=16, k=4, I=128, S=1, Is=128, dtype=moe.MOE_BF16)
+    base.update(kw)
+    return moe.MoEShape(*[base[n] for n, _ in moe.MoEShape._fields_])
+
+
+def opts(**kw):
+    base = dict(score=0, groups=4, top_groups=2, group_top=2, renormalize=1, scale=1.0)
+    base.update(kw)
+    return moe.MoERouteOpts(*[base[n] for n, _ in moe.MoERouteOpts._fields_])
+
+
+def c(v):
+    return None if v is None else ctypes.c_void_p(v)
+
+
+def _route(L, sh, o, **ptr):
+    p = dict(z=FAKE, bias=FAKE, idx=FAKE, w=FAKE, counts=FAKE)
+    p.update(ptr)
+    return L.moe_route_logits(c(p["z"]), c(p["bias"]), sh, o, c(p["idx"]), c(p["w"]), c(p["counts"]), None)
+
+
+def _route_bwd(L, sh, o, **ptr):
+    p = dict(z=FAKE, idx=FAKE, dw=FAKE, ds=None, dz=FAKE)
+    p.update(ptr)
+    return L.moe_route_logits_backward(c(p["z"]), c(p["idx"]), c(p["dw"]), c(p["ds"]), sh, o, c(p["dz"]), None)
+
+
+BAD_OPTS = [
+    (dict(score=2), INVALID), (dict(score=-1), INVALID), (dict(groups=0), INVALID), (dict(groups=5), INVALID),
+    (dict(top_groups=0), INVALID), (dict(top_groups=5), INVALID), (dict(group_top=0), INVALID),
+    (dict(group_top=3), INVALID), (dict(renormalize=2), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(groups=16, top_groups=3), INVALID),  # 3 experts kept, 4 wanted
+]
+
+
+@pytest.mark.parametrize("bad,code", BAD_OPTS)
+def test_route_refuses_bad_options(L, bad, code):
+    assert _route(L, shape(), opts(**bad)) == code
+    assert _route_bwd(L, shape(), opts(**bad)) == code
+
+
+def test_route_refuses_too_many_groups(L):
+    assert _route(L, shape(E=64), opts(groups=64, top_groups=8)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(k=0), INVALID), (dict(k=17, E=32), UNSUPPORTED), (dict(k=5, E=4), INVALID), (dict(E=300), UNSUPPORTED),
+    (dict(T=-1), INVALID), (dict(dtype=7), INVALID),
+])
+def test_route_refuses_bad_shapes(L, bad, code):
+    o = opts(groups=1, top_groups=1)
+    assert _route(L, shape(**bad), o) == code
+    assert _route_bwd(L, shape(**bad), o) == code
+
+
+@pytest.mark.parametrize("name", ["z", "idx", "w", "counts"])
+def test_route_refuses_null_and_misaligned(L, name):
+    assert _route(L, shape(), opts(), **{name: None}) == INVALID
+    assert _route(L, shape(), opts(), **{name: FAKE + 8}) == ALIGN
+
+
+@pytest.mark.parametrize("name", ["z", "idx", "dw", "dz"])
+def test_route_backward_refuses_null_and_misaligned(L, name):
+    assert _route_bwd(L, shape(), opts(), **{name: None}) == INVALID
+    assert _route_bwd(L, shape(), opts(), **{name: FAKE + 4}) == ALIGN
+    assert _route_bwd(L, shape(), opts(), ds=FAKE + 4) == ALIGN
+
+
+def test_gate_logits_refusals(L):
+    f = lambda sh, x=FAKE, w=FAKE, z=FAKE: L.moe_gate_logits(c(x), c(w), sh, c(z), None)
+    assert f(shape(), x=None) == INVALID and f(shape(), w=None) == INVALID and f(shape(), z=None) == INVALID
+    assert f(shape(), z=FAKE + 4) == ALIGN and f(shape(), x=FAKE + 2) == ALIGN
+    assert f(shape(d=96)) == UNSUPPORTED
+
+
+def _saved(**kw):
+    p = {n: FAKE for n, _ in moe.MoESavedActs._fields_}
+    p.update(kw)
+    return moe.MoESavedActs(**p)
+
+
+def _up(L, sh, saved, x=FAKE, h=FAKE, hs=FAKE, ws1=FAKE):
+    return L.moe_ffn_up_save(c(FAKE), c(FAKE), c(FAKE), c(FAKE), c(x), c(ws1), c(FAKE), sh, c(h), c(hs),
+                             ctypes.byref(saved) if saved is not None else None, None)
+
+
+def test_up_save_refusals(L):
+    assert _up(L, shape(), None) == INVALID
+    for name, _ in moe.MoESavedActs._fields_:
+        assert _up(L, shape(), _saved(**{name: None})) == INVALID, name
+        assert _up(L, shape(), _saved(**{name: FAKE + 8})) == ALIGN, name
+    assert _up(L, shape(), _saved(), h=None) == INVALID
+    assert _up(L, shape(), _saved(), hs=None) == INVALID
+    assert _up(L, shape(), _saved(), ws1=None) == INVALID
+    assert _up(L, shape(dtype=moe.MOE_F32), _saved()) == UNSUPPORTED
+    assert _up(L, shape(dtype=moe.MOE_FP8_E4M3), _saved()) == UNSUPPORTED
+    assert _up(L, shape(I=96), _saved()) == UNSUPPORTED
+
+
+def _bwd(L, sh, saved, expert_set=0, **ptr):
+    p = dict(u=FAKE, perm=FAKE, w=FAKE, dadg=FAKE, h=None, dw=FAKE)
+    p.update(ptr)
+    return L.moe_swiglu_backward_saved(ctypes.byref(saved) if saved is not None else None, sh, expert_set, c(p["u"]),
+                                       c(p["perm"]), c(p["w"]), c(p["dadg"]), c(p["h"]), c(p["dw"]), None)
+
+
+def test_swiglu_backward_refusals(L):
+    assert _bwd(L, shape(), None) == INVALID
+    assert _bwd(L, shape(), _saved(), expert_set=2) == INVALID
+    assert _bwd(L, shape(S=0), _saved(), expert_set=1) == INVALID
+    for name in ("u", "perm", "w", "dadg", "dw"):
+        assert _bwd(L, shape(), _saved(), **{name: None}) == INVALID, name
+        assert _bwd(L, shape(), _saved(), **{name: FAKE + 8}) == ALIGN, name
+    assert _bwd(L, shape(), _saved(), h=FAKE + 8) == ALIGN
+    for name in ("a", "a_scale", "g", "g_scale"):
+        assert _bwd(L, shape(), _saved(**{name: None})) == INVALID
+    for name in ("sa", "sa_scale", "sg", "sg_scale"):
+        assert _bwd(L, shape(), _saved(**{name: None}), expert_set=1) == INVALID
+    assert _bwd(L, shape(dtype=moe.MOE_F32), _saved()) == UNSUPPORTED
+
+
+def test_binding_helpers():
+    with pytest.raises(ValueError):
+        moe.route_opts("relu")
+    o = moe.route_opts("softmax", groups=8, top_groups=3, renormalize=False, scale=16.0)
+    assert (o.score, o.groups, o.top_groups, o.group_top, o.renormalize, o.scale) == (1, 8, 3, 1, 0, 16.0)
+    buf = moe.saved_act_buffers(shape(S=0), "cpu")
+    assert set(buf) == {"a", "a_scale", "g", "g_scale"}
+    assert buf["a"].shape == (512, 128) and buf["a_scale"].numel() == 512 * 4
+    buf = moe.saved_act_buffers(shape(S=2), "cpu")
+    assert buf["sg"].shape == (128, 256) and buf["sg_scale"].numel() == 2 * 128 * 4
+    s = moe.saved_acts(buf)
+    assert s.sa == buf["sa"].data_ptr()
