@@ -844,7 +844,7 @@ moe_status moe_route_logits_backward(const float* logits, const int32_t* topk_id
     v = device_setup(&dev, &status, &sms);
     if (v != MOE_OK) return v;
     return moe::launch_route_logits_bwd(logits, topk_idx, dw, dscores, sh.T, sh.E, sh.k, route_opts(opts), dlogits,
-                                        status, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                                        status, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }

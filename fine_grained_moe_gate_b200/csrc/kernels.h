@@ -85,7 +85,7 @@ struct RouteOpts {
 cudaError_t launch_route_logits(const float* logits, const float* bias, int T, int E, int k, const RouteOpts& o,
                                 int32_t* idx, float* w, int32_t* counts, int* status, int num_sms, cudaStream_t st);
 cudaError_t launch_route_logits_bwd(const float* logits, const int32_t* idx, const float* dw, const float* dscores,
-                                    int T, int E, int k, const RouteOpts& o, float* dlogits, int* status, int num_sms,
+                                    int T, int E, int k, const RouteOpts& o, float* dlogits, int* status,
                                     cudaStream_t st);
 
 // act_save.cu: the SwiGLU backward from saved 8-bit pre-activations.  Codes
