@@ -35,6 +35,14 @@ __device__ __forceinline__ float warp_max(float v) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ int ld_cluster_i32(uint32_t cluster_addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+// Programmatic dependent launch: waits until the kernel before this one on
+// the stream is complete and its writes are visible.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ double warp_max(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, o));
@@ -77,6 +85,7 @@ struct alignas(16) WarpMem {
     double d[kMaxExperts];        // 64-bit values, or all experts' 32-bit values
     Cand cand[kMaxExperts + 2];   // in any order
     Cand sorted[kMaxK + 2];       // the k + 1 best, descending
+    int first[32];                // first expert of each kept group
 };
 static_assert(sizeof(WarpMem) % 16 == 0, "vector reads in every warp's copy");
 
@@ -84,7 +93,10 @@ struct RouteArgs {
     const float* logits;
     const float* bias;
     int T, E, k;
-    int per_inv;  // ceil(2^16 / experts of a group): e / per = e per_inv >> 16 for e, per <= 256
+    int per;           // experts of a group
+    int per_inv;       // ceil(2^16 / per): e / per = e per_inv >> 16 for e, per <= 256
+    int group_lanes;   // lanes that take a group's values, a power of two
+    unsigned leaders;  // lane g group_lanes of every group g
     RouteOpts o;
     int32_t* idx;
     float* w;
@@ -160,16 +172,21 @@ __device__ __noinline__ void sort_candidates64(const RouteArgs& a, const float* 
     __syncwarp();
 }
 
-// The share of each lane's chosen logit in the sum over the chosen scores
-// (lanes without one: live false).  s = e^min(z,0) / (1 + e^-|z|) (sigmoid) or
-// e^z / const (softmax), with the largest exponent taken out of the ratio, so
-// that it stands where every score underflows.
+// The share of each lane's chosen logit in the sum over the chosen scores of
+// its SLOTS lanes (lanes without one: live false).  s = e^min(z,0) / (1 +
+// e^-|z|) (sigmoid) or e^z / const (softmax), with the largest exponent taken
+// out of the ratio, so that it stands where every score underflows.
+template <int SLOTS>
 __device__ __forceinline__ float chosen_share(float z, bool live, bool softmax) {
     const float x = softmax ? z : fminf(z, 0.0f);
-    const float m = warp_max(live ? x : neg_inf());
+    float m = live ? x : neg_inf();
+#pragma unroll
+    for (int o = SLOTS / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     float p = live ? (x == m ? 1.0f : expf(x - m)) : 0.0f;
     if (!softmax && live) p = __fdividef(p, 1.0f + expf(-fabsf(z)));
-    const float tot = warp_sum(p);
+    float tot = p;
+#pragma unroll
+    for (int o = SLOTS / 2; o > 0; o >>= 1) tot += __shfl_xor_sync(kFull, tot, o);
     return tot > 0.0f ? __fdividef(p, tot) : 0.0f;
 }
 
@@ -188,10 +205,9 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // k, and its row only E floats.  So the scores that only decide the choice use
 // the hardware's exponential and reciprocal (2 instructions each), and the
 // accurate ones are left to the k chosen, one per lane.  A value's low three
-// bits are replaced by its register's number j (expert lane + 32 j), so that
-// values alone are compared and moved.  Every lane keeps its three best; k + 1
+// bits are replaced by its register's number j, so that values alone are compared and moved.  Every lane sorts its four best; k + 1
 // warp maxima take the best values in descending order, the lane that owns one
-// moves its next up.  Where a lane would need its fourth, or two values are
+// moves its next up.  Where a lane would need its fifth, or two values are
 // equal, all values from the threshold found up are compacted and ranked by
 // counting instead.
 //
@@ -205,80 +221,104 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // the rounding of v and its low bits, 16u (|v_a| + |v_b|).  A group's value
 // sums two.  1e-37 covers what is below the normal range.
 constexpr float kRelErr = 0x1p-16f, kAbsErr = 0x1p-19f, kSumErr = 0x1p-20f;
+constexpr float kLog2e = 1.4426950408889634f, kFltMax = 3.4028234664e38f;
+// A masked value, and the bound below which a value is one.  Finite biases are
+// held above it (those beyond -1e37 tie in 32 bits and are compared in 64).
+constexpr float kMasked = -kFltMax, kLow = -1e38f;
 
 // v with its low three bits replaced by j.
 __device__ __forceinline__ float tagged(float v, int j) {
     return __uint_as_float((__float_as_uint(v) & ~7u) | (uint32_t)j);
 }
 
-// x1 >= x2 >= x3, the largest so far, with y among them.
-__device__ __forceinline__ void insert3(float& x1, float& x2, float& x3, float y) {
-    const float t = fminf(x1, y), u = fminf(x2, t);
-    x1 = fmaxf(x1, y);
-    x2 = fmaxf(x2, t);
-    x3 = fmaxf(x3, u);
+__device__ __forceinline__ void order(float& a, float& b) {  // a >= b
+    const float t = fminf(a, b);
+    a = fmaxf(a, b);
+    b = t;
+}
+__device__ __forceinline__ void sort4(float (&x)[4]) {
+    order(x[0], x[1]);
+    order(x[2], x[3]);
+    order(x[0], x[2]);
+    order(x[1], x[3]);
+    order(x[1], x[2]);
+}
+// The four largest so far, descending, with y among them.
+__device__ __forceinline__ void insert4(float (&x)[4], float y) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) order(x[i], y);
+}
+// The four largest of v, descending.
+template <int VPT>
+__device__ __forceinline__ void best4(const float (&v)[VPT], float (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = i < VPT ? v[i < VPT ? i : 0] : kMasked;
+    if (VPT == 2) order(x[0], x[1]);
+    if (VPT >= 4) sort4(x);
+    if (VPT == 8) {
+        float y[4] = {v[4 % VPT], v[5 % VPT], v[6 % VPT], v[7 % VPT]};
+        sort4(y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmaxf(x[i], y[3 - i]);  // the four largest, rising then falling
+        order(x[0], x[2]);
+        order(x[1], x[3]);
+        order(x[0], x[1]);
+        order(x[2], x[3]);
+    }
 }
 
-// The best two of each register over the warp: in steps that halve the
-// registers, lane l ends with the pair of register l / (32 / VPT).
+// The two largest of v, x1 >= x2 (VPT 1: x2 masked).
 template <int VPT>
-__device__ __forceinline__ void best2_by_register(const float (&v)[VPT], int lane, float& x1, float& x2) {
-    float a1[VPT], a2[VPT];
+__device__ __forceinline__ void best2(const float (&v)[VPT], float& x1, float& x2) {
+    float hi[VPT], lo[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT / 2; ++j) {
+        hi[j] = fmaxf(v[2 * j], v[2 * j + 1 < VPT ? 2 * j + 1 : 0]);
+        lo[j] = fminf(v[2 * j], v[2 * j + 1 < VPT ? 2 * j + 1 : 0]);
+    }
+    if (VPT == 1) {
+        hi[0] = v[0];
+        lo[0] = kMasked;
+    }
+#pragma unroll
+    for (int n = VPT / 4; n > 0; n /= 2)
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            lo[j] = fmaxf(fminf(hi[j], hi[j + n]), fmaxf(lo[j], lo[j + n]));
+            hi[j] = fmaxf(hi[j], hi[j + n]);
+        }
+    x1 = hi[0];
+    x2 = lo[0];
+}
+
+// Where candidates begin below the (k + 1)-th value found.
+__device__ __forceinline__ float cut_of(float best, float abs_err, float rel_err) {
+    return fmaxf(best - (abs_err + 2.0f * rel_err * fabsf(best) + 1e-37f), kLow);
+}
+
+// The general way to the k + 1 best: all values of the kept groups (bit g LG
+// of kept) from cut up, compacted and ranked by counting.  Returns whether two
+// of them are equal; n: how many.
+template <int VPT>
+__device__ __noinline__ bool rank_candidates(const RouteArgs& a, const float (&v)[VPT], unsigned kept, int LG, float cut,
+                                             WarpMem& wm, int lane, int& n) {
+    unsigned in = 0u;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        a1[j] = v[j];
-        a2[j] = neg_inf();
+        const int g = (lane * VPT + j) * a.per_inv >> 16;
+        if (v[j] >= cut && ((kept >> ((g * LG) & 31)) & 1u)) in |= 1u << j;
     }
-    int n = VPT;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (n > 1) {  // the upper half of the lanes takes the upper half of the registers
-            n /= 2;
-            const bool up = lane & o;
-#pragma unroll
-            for (int j = 0; j < VPT / 2; ++j)
-                if (j < n) {
-                    const int h = j + n < VPT ? j + n : j;
-                    const float y1 = __shfl_xor_sync(kFull, up ? a1[j] : a1[h], o);
-                    const float k1 = up ? a1[h] : a1[j];
-                    if (o == 16) {  // first step: no second values yet
-                        a1[j] = fmaxf(k1, y1);
-                        a2[j] = fminf(k1, y1);
-                    } else {
-                        const float y2 = __shfl_xor_sync(kFull, up ? a2[j] : a2[h], o);
-                        const float k2 = up ? a2[h] : a2[j];
-                        a2[j] = fmaxf(fminf(k1, y1), fmaxf(k2, y2));
-                        a1[j] = fmaxf(k1, y1);
-                    }
-                }
-        } else {
-            const float y1 = __shfl_xor_sync(kFull, a1[0], o), y2 = __shfl_xor_sync(kFull, a2[0], o);
-            a2[0] = fmaxf(fminf(a1[0], y1), fmaxf(a2[0], y2));
-            a1[0] = fmaxf(a1[0], y1);
-        }
-    }
-    x1 = a1[0];
-    x2 = a2[0];
-}
-
-// The general way to the k + 1 best: all values from cut up, compacted and
-// ranked by counting.  Returns whether two of them are equal; n: how many.
-template <int VPT>
-__device__ __noinline__ bool rank_candidates(const float (&v)[VPT], float cut, int k, WarpMem& wm, int lane, int& n) {
-    int mine = 0;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) mine += v[j] >= cut;
-    int pos = mine;
+    int pos = __popc(in);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(kFull, pos, o);
         if (lane >= o) pos += x;
     }
     n = __shfl_sync(kFull, pos, 31);
-    pos -= mine;
+    pos -= __popc(in);
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
-        if (v[j] >= cut) wm.cand[pos++] = Cand{v[j], lane + 32 * j};
+        if ((in >> j) & 1u) wm.cand[pos++] = Cand{v[j], lane * VPT + j};
     if (lane == 0) wm.cand[n].v = neg_inf();
     __syncwarp();
     bool equal = false;
@@ -290,7 +330,7 @@ __device__ __noinline__ bool rank_candidates(const float (&v)[VPT], float cut, i
             rank += (y.x > x.v) + (y.z > x.v);
             upto += (y.x >= x.v) + (y.z >= x.v);
         }
-        if (rank <= k) {
+        if (rank <= a.k) {
             wm.sorted[rank] = x;
             equal |= upto - rank > 1;
         }
@@ -298,181 +338,228 @@ __device__ __noinline__ bool rank_candidates(const float (&v)[VPT], float cut, i
     return equal;
 }
 
-// Lane l holds experts l, l + 32, ...: the experts of one group lie in as many
-// lanes as they can, which keeps the lanes' best values distinct experts of
-// the kept groups (with runs of experts in a lane, 4 kept groups of 32 filled
-// 16 lanes and left three times the candidates).
-template <int VPT, bool SOFTMAX, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 4 : 1) route_logits_kernel(const __grid_constant__ RouteArgs a) {
+// Lane l holds experts [l VPT, (l + 1) VPT).  Grouped choices list the kept
+// groups' experts again over all lanes, so that no lane holds many of them.
+// SMALL: one cluster takes the batch and adds its CTAs' counts itself;
+// otherwise counts were cleared by the kernel before this one on the stream.
+template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
+__global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
+    route_logits_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
     int* hist = reinterpret_cast<int*>(smem + WARPS * sizeof(WarpMem));
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int E = a.E, k = a.k;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int E = a.E, k = a.k, e0 = lane * VPT;
     for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
     __syncthreads();
 
-    // Groups.  LG lanes of a warp take a group's values from shared memory;
-    // a group of 32 experts is one register of the warp, and its best two
-    // values meet by shuffles in LG lanes.
-    const bool grouped = a.o.top_groups < a.o.groups;
-    const int per = E / a.o.groups;
-    const bool in_rows = per == 32 && a.o.groups * 2 > VPT;
-    int LG = in_rows ? 32 / VPT : 1;
-    if (!in_rows)
-        while (2 * LG * a.o.groups <= 32) LG *= 2;
-    const int my_group = lane / LG;
+    const bool vec = (E & 3) == 0;
     float b[VPT];
-    unsigned gbit[VPT];  // the bit of each expert's group (group g: bit g LG)
+    bool odd = false;  // a bias that masks or forces
+    load_row<VPT>(a.bias ? a.bias : a.logits, e0, a.bias ? E : 0, vec, 0.0f, b);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int e = lane + 32 * j;
-        b[j] = a.bias && e < E ? a.bias[e] : 0.0f;
         if (b[j] != b[j]) {  // masked, and reported
             b[j] = neg_inf();
             report(a.status, kStDeviceCheck);
         }
-        b[j] = fminf(b[j], 3.4028235e38f);  // +inf: compared in 64 bits
-        gbit[j] = grouped ? 1u << (((e * a.per_inv >> 16) * LG) & 31) : 0u;  // e / per
+        odd |= fabsf(b[j]) > kFltMax;
+        if (b[j] != neg_inf()) b[j] = fmaxf(fminf(b[j], kFltMax), -1e37f);
+        if (e0 + j >= E) b[j] = kMasked;
     }
+    odd = __any_sync(kFull, odd);
+    // Groups: LG lanes take a group's values, from their registers where a
+    // group is a power of two of whole lanes, else from shared memory.
+    const bool grouped = a.o.top_groups < a.o.groups;
+    const int per = a.per, LG = a.group_lanes;
+    const bool in_lanes = LG * VPT == per;
+    const int my_group = lane / LG, sub = lane & (LG - 1);
+    const bool real = my_group < a.o.groups;
 
-    for (int t = blockIdx.x * WARPS + (tid >> 5); t < a.T; t += gridDim.x * WARPS) {
+    for (int t = SMALL ? warp * gridDim.x + blockIdx.x : blockIdx.x * WARPS + warp; t < a.T; t += gridDim.x * WARPS) {
         const float* row = a.logits + (size_t)t * E;
         float v[VPT];
+        load_row<VPT>(row, e0, E, vec, kMasked, v);
+        float nf = 0.0f;  // NaN where a logit is not finite
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) v[j] = lane + 32 * j < E ? row[lane + 32 * j] : neg_inf();
-        bool bad = false;
+        for (int j = 0; j < VPT; ++j) nf = fmaf(v[j], 0.0f, nf);
+        bool special = nf != nf;
         float m = 0.0f, top = 1.0f;  // softmax: the largest logit; a bound of the scores
         if (SOFTMAX) {
-            m = neg_inf();
+            m = v[0];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                bad |= v[j] != v[j];
-                v[j] = fmaxf(v[j], neg_inf());  // NaN: masked
-                m = fmaxf(m, v[j]);
-            }
+            for (int j = 1; j < VPT; ++j) m = fmaxf(m, v[j]);  // NaN drops out
             m = warp_max(m);
-            const float ref = fabsf(m) < __int_as_float(0x7f800000) ? m : 0.0f;
-            float part = 0.0f, s[VPT];
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) s[j] = ex2_fast((v[j] - ref) * 1.4426950408889634f);
-            if (m > 3.4e38f)  // logit +inf
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) s[j] = v[j] == m ? 1.0f : 0.0f;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) part += s[j];
-            top = rcp_fast(fmaxf(warp_sum(part), 1e-30f));
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const float x = tagged(fmaf(s[j], top, b[j]), j);
-                v[j] = v[j] == neg_inf() || b[j] == neg_inf() ? neg_inf() : x;
-            }
-        } else {
+            special |= !(m > kLow);
+        }
+        special = __any_sync(kFull, special) || odd;  // masks, infinities, NaN: the long way
+        bool bad = false;
+        unsigned masked = 0u;
+        if (special) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 bad |= v[j] != v[j];
-                const float x = tagged(rcp_fast(1.0f + ex2_fast(v[j] * -1.4426950408889634f)) + b[j], j);
-                v[j] = v[j] > neg_inf() && b[j] > neg_inf() ? x : neg_inf();
+                if (!(v[j] > neg_inf()) || b[j] == neg_inf() || e0 + j >= E) masked |= 1u << j;
+                if (!(v[j] > neg_inf()) || e0 + j >= E) v[j] = neg_inf();
             }
         }
+        if (SOFTMAX) {
+            float part = 0.0f;
+            if (special) {
+                const float ref = fabsf(m) <= kFltMax ? m : 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    const float z = v[j];
+                    v[j] = ex2_fast((z - ref) * kLog2e);
+                    if (m > kFltMax) v[j] = z == m ? 1.0f : 0.0f;  // logit +inf
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) v[j] = ex2_fast((v[j] - m) * kLog2e);
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) part += v[j];
+            top = rcp_fast(fmaxf(warp_sum(part), 1e-30f));
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) v[j] = tagged(fmaf(v[j], top, b[j]), j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) v[j] = tagged(rcp_fast(1.0f + ex2_fast(v[j] * -kLog2e)) + b[j], j);
+        }
+        if (special)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if ((masked >> j) & 1u) v[j] = kMasked;
         const float abs_err = a.bias ? top * kAbsErr : 0.0f, rel_err = a.bias ? kSumErr : kRelErr;
 
+        float x[4] = {kMasked, kMasked, kMasked, kMasked};
+        unsigned kept = a.leaders;
+        int held = VPT;  // values that went into x
         if (grouped) {
-            float x1 = neg_inf(), x2 = neg_inf();
-            if (in_rows) {
-                best2_by_register<VPT>(v, lane, x1, x2);
-            } else {
-                float* all = reinterpret_cast<float*>(wm.d);
+            float* all = reinterpret_cast<float*>(wm.d);
+            const auto put = [&] {  // the row's values where every lane can read them
+                if (VPT % 4 == 0) {
 #pragma unroll
-                for (int j = 0; j < VPT; ++j)
-                    if (lane + 32 * j < E) all[lane + 32 * j] = v[j];
+                    for (int j = 0; j < VPT; j += 4)
+                        *reinterpret_cast<float4*>(all + e0 + j) =
+                            make_float4(v[j], v[j + 1 < VPT ? j + 1 : j], v[j + 2 < VPT ? j + 2 : j],
+                                        v[j + 3 < VPT ? j + 3 : j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VPT; ++j) all[e0 + j] = v[j];
+                }
                 __syncwarp();
-                if (my_group < a.o.groups) {
-                    const int first = my_group * per, last = first + per;
-                    for (int i = first + (lane & (LG - 1)); i < last; i += LG) {
-                        const float x = all[i];
-                        x2 = fmaxf(x2, fminf(x1, x));
-                        x1 = fmaxf(x1, x);
-                    }
-                }
-                for (int o = 1; o < LG; o <<= 1) {
-                    const float y1 = __shfl_xor_sync(kFull, x1, o), y2 = __shfl_xor_sync(kFull, x2, o);
-                    x2 = fmaxf(fminf(x1, y1), fmaxf(x2, y2));
-                    x1 = fmaxf(x1, y1);
-                }
-            }
-            float gv = a.o.group_top == 2 && x2 > neg_inf() ? x1 + x2 : x1;
-            // the best groups leave one by one; lo: the last kept, hi: the best left
-            bool keep = false;
-            float lo = neg_inf();
-            for (int r = 0; r < a.o.top_groups; ++r) {
-                lo = warp_max(gv);
-                if (gv == lo && lo > neg_inf()) {
-                    keep = true;
-                    gv = neg_inf();
+            };
+            put();
+            float x1 = kMasked, x2 = kMasked;
+            if (in_lanes) {
+                best2<VPT>(v, x1, x2);
+            } else if (real) {
+                const int last = (my_group + 1) * per;
+                for (int i = my_group * per + sub; i < last; i += LG) {
+                    const float y = all[i];
+                    x2 = fmaxf(x2, fminf(x1, y));
+                    x1 = fmaxf(x1, y);
                 }
             }
-            const float hi = warp_max(gv);
-            unsigned kept = __ballot_sync(kFull, keep);  // bit g LG (and the group's other lanes)
-            const float gerr = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
-            if (__popc(kept) > a.o.top_groups * LG || (hi > neg_inf() && !(lo - hi > gerr)))  // equal, or too close
+            for (int o = 1; o < LG; o <<= 1) {
+                const float y1 = __shfl_xor_sync(kFull, x1, o), y2 = __shfl_xor_sync(kFull, x2, o);
+                x2 = fmaxf(fminf(x1, y1), fmaxf(x2, y2));
+                x1 = fmaxf(x1, y1);
+            }
+            float gv = a.o.group_top == 2 && x2 > kLow ? x1 + x2 : x1;
+            if (!real) gv = kMasked;
+            // a group's lanes share the comparison with the others
+            const float err = 3.0f * abs_err + 2.0f * rel_err * fabsf(gv) + 1e-37f;
+            int ahead = 0;
+            bool unsure = false;
+            for (int i = 0; i < a.o.groups; i += LG) {
+                const float y = __shfl_sync(kFull, gv, ((i + sub) * LG) & 31);
+                const bool other = i + sub < a.o.groups && i + sub != my_group && y > kLow;
+                ahead += other && y > gv;
+                unsure |= other && !(fabsf(y - gv) > fmaf(2.0f * rel_err, fabsf(y), err));
+            }
+            for (int o = 1; o < LG; o <<= 1) ahead += __shfl_xor_sync(kFull, ahead, o);
+            kept = __ballot_sync(kFull, gv > kLow && ahead < a.o.top_groups) & a.leaders;
+            if (__any_sync(kFull, unsure && gv > kLow)) {
                 kept = kept_groups64(a, row, wm, LG, lane);
+                __syncwarp();
+                put();  // it took the values' room
+            }
+            // the kept groups' experts in a row, 32 at a time
+            if ((kept >> lane) & 1u) wm.first[__popc(kept & ((1u << lane) - 1u))] = my_group * per;
+            __syncwarp();
+            const int count = __popc(kept) * per;
+            held = (count + 31) >> 5;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) v[j] = (kept & gbit[j]) ? v[j] : neg_inf();
+            for (int i = 0; i < VPT; ++i)
+                if (i < held) {
+                    const int q = lane + 32 * i, g = q * a.per_inv >> 16;
+                    float y = kMasked;
+                    if (q < count) y = tagged(all[wm.first[g] + q - g * per], i);
+                    insert4(x, y);
+                }
+        } else {
+            best4<VPT>(v, x);
         }
 
         // the k + 1 best in descending order
-        float x1 = v[0], x2 = neg_inf(), x3 = neg_inf();
-#pragma unroll
-        for (int j = 1; j < VPT; ++j) insert3(x1, x2, x3, v[j]);
         __syncwarp();  // the last token's readers are done
-        int n = 0, taken = 0;
-        float thr = neg_inf();
+        float best = kMasked;
+        int taken = 0;
 #pragma unroll 3
         for (int r = 0; r <= k; ++r) {
-            const float best = warp_max(x1);
-            if (!(best > neg_inf())) {
-                thr = neg_inf();
-                break;
-            }
-            thr = best;
-            if (x1 == best) {
-                wm.sorted[r] = Cand{best, lane};
-                x1 = x2;
-                x2 = x3;
-                x3 = neg_inf();
-                ++taken;
-            }
-            ++n;
+            best = warp_max(x[0]);
+            const bool own = x[0] == best;
+            if (own) wm.sorted[r] = Cand{best, lane};
+            x[0] = own ? x[1] : x[0];
+            x[1] = own ? x[2] : x[1];
+            x[2] = own ? x[3] : x[2];
+            x[3] = own ? kMasked : x[3];
+            taken += own;
         }
-        bool close = false;
-        if (__reduce_add_sync(kFull, VPT > 3 && taken >= 3 ? 1000 : taken) != n) {
-            const float cut = fmaxf(thr - (abs_err + 2.0f * rel_err * fabsf(thr) + 1e-37f), -3.4028235e38f);
-            close = rank_candidates<VPT>(v, cut, k, wm, lane, n);
+        // every round one lane's, and no lane's fifth wanted
+        bool close = false, ranked = false;
+        int n = k + 1;
+        if (__reduce_add_sync(kFull, held > 4 && taken >= 4 ? 1000 : taken) != k + 1 || !(best > kLow)) {
+            close = rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
+            ranked = true;
         }
         __syncwarp();
         if (lane < k && lane + 1 < n) {
-            const float x = wm.sorted[lane].v, y = wm.sorted[lane + 1].v;
-            close |= !(x - y > abs_err + rel_err * (fabsf(x) + fabsf(y)) + 1e-37f);
+            const float y0 = wm.sorted[lane].v, y1 = wm.sorted[lane + 1].v;
+            close |= !(y0 - y1 > abs_err + rel_err * (fabsf(y0) + fabsf(y1)) + 1e-37f);
         }
-        const bool live = lane < k && lane < n;
-        int e = live ? (int)(__float_as_uint(wm.sorted[lane].v) & 7u) * 32 + (wm.sorted[lane].e & 31) : -1;
         if (__any_sync(kFull, close)) {
-            const float cut = fmaxf(thr - (abs_err + 2.0f * rel_err * fabsf(thr) + 1e-37f), -3.4028235e38f);
-            rank_candidates<VPT>(v, cut, k, wm, lane, n);
+            if (!ranked) rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
+            ranked = true;
             __syncwarp();
             sort_candidates64(a, row, wm, n, lane);
-            if (live) e = wm.sorted[lane].e;
+        }
+        const bool live = lane < k && lane < n;
+        int e = -1;
+        if (live) {
+            const Cand c = wm.sorted[lane];
+            e = c.e;
+            if (!ranked) {  // the value's lane; its low bits: the register
+                const int j = (int)(__float_as_uint(c.v) & 7u);
+                if (grouped) {
+                    const int q = e + 32 * j, g = q * a.per_inv >> 16;
+                    e = wm.first[g] + q - g * per;
+                } else {
+                    e = e * VPT + j;
+                }
+            }
         }
         const float z = live ? row[e] : 0.0f;
-        float x;
+        float wt;
         if (a.o.renormalize)
-            x = chosen_share(z, live, SOFTMAX);
+            wt = k <= 8 ? chosen_share<8>(z, live, SOFTMAX) : chosen_share<16>(z, live, SOFTMAX);
         else
-            x = !live ? 0.0f : SOFTMAX ? (z == m ? top : expf(z - m) * top) : __fdividef(1.0f, 1.0f + expf(-z));
+            wt = !live ? 0.0f : SOFTMAX ? (z == m ? top : expf(z - m) * top) : __fdividef(1.0f, 1.0f + expf(-z));
         if (lane < k) {
             a.idx[(size_t)t * k + lane] = e;
-            a.w[(size_t)t * k + lane] = x * a.o.scale;
+            a.w[(size_t)t * k + lane] = wt * a.o.scale;
             if (live)
                 atomicAdd(&hist[e], 1);
             else
@@ -480,13 +567,28 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 4 : 1) route_logits_k
         }
         if (bad) report(a.status, kStDeviceCheck);
     }
-    __syncthreads();
-    if (gridDim.x == 1) {  // the whole batch in this CTA: no cleared counters needed
-        for (int e = tid; e < E; e += WARPS * 32) a.counts[e] = hist[e];
+    if (SMALL) {
+        cluster_sync_all();  // every CTA's counts are in
+        const unsigned n_ctas = gridDim.x;
+        for (int e = blockIdx.x * WARPS * 32 + tid; e < E; e += n_ctas * WARPS * 32) {
+            int c = 0;
+            for (unsigned r = 0; r < n_ctas; ++r) c += ld_cluster_i32(mapa_shared(smem_u32(hist + e), r));
+            a.counts[e] = c;
+        }
+        cluster_sync_all();  // no CTA leaves while its counts are read
     } else {
+        __syncthreads();
+        grid_dependency_wait();  // the counters are clear
         for (int e = tid; e < E; e += WARPS * 32)
             if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
     }
+}
+
+// Clears the counters.  The routing kernel may start beside it (it waits for
+// this kernel's end before it adds).
+__global__ void clear_counts_kernel(int32_t* counts, int E) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int e = threadIdx.x; e < E; e += blockDim.x) counts[e] = 0;
 }
 
 // ---------------------------------------------------------------- backward
@@ -504,9 +606,8 @@ struct RouteBwdArgs {
 
 constexpr int kBwdWarps = 8;
 
-// DENSE: every expert's score is needed (dscores, or softmax as scored);
-// otherwise only the chosen logits are read.
-template <int VPT, bool DENSE>
+// Every expert's score is needed (dscores, or softmax as scored).
+template <int VPT>
 __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_kernel(const __grid_constant__ RouteBwdArgs a) {
     __shared__ __align__(16) float rows[kBwdWarps][32 * VPT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -518,14 +619,12 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_kernel(const 
     float* add = rows[warp];  // what the chosen slots add: to dz, or to ds (softmax as scored)
 
     float s[VPT], ds[VPT];
-    if (DENSE) {
-        load_row<VPT>(row, e0, E, vec, neg_inf(), s);
-        if (a.dscores)
-            load_row<VPT>(a.dscores + (size_t)t * E, e0, E, vec, 0.0f, ds);
-        else
+    load_row<VPT>(row, e0, E, vec, neg_inf(), s);
+    if (a.dscores)
+        load_row<VPT>(a.dscores + (size_t)t * E, e0, E, vec, 0.0f, ds);
+    else
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) ds[j] = 0.0f;
-    }
+        for (int j = 0; j < VPT; ++j) ds[j] = 0.0f;
     // chosen slots
     int e = -1;
     float G = 0.0f, z = neg_inf();
@@ -543,7 +642,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_kernel(const 
     const bool live = e >= 0 && z > neg_inf();  // not masked, not NaN
     float c = 0.0f;
     if (a.o.renormalize) {
-        const float p = chosen_share(z, live, softmax);
+        const float p = chosen_share<32>(z, live, softmax);
         const float dot = warp_sum(live ? G * p : 0.0f);
         if (live) c = p * (G - dot) * (softmax ? 1.0f : __fdividef(1.0f, 1.0f + expf(z)));
     } else if (softmax) {
@@ -573,38 +672,36 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_kernel(const 
 #pragma unroll
     for (int j = 0; j < VPT; ++j) dz[j] = 0.0f;
     load_row<VPT>(add, e0, 32 * VPT, true, 0.0f, dz);
-    if (DENSE) {
-        if (softmax) {
-            float m = neg_inf();
+    if (softmax) {
+        float m = neg_inf();
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) m = fmaxf(m, s[j]);
-            m = warp_max(m);
-            float part = 0.0f, dot = 0.0f;
+        for (int j = 0; j < VPT; ++j) m = fmaxf(m, s[j]);
+        m = warp_max(m);
+        float part = 0.0f, dot = 0.0f;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const bool in = s[j] > neg_inf();
-                s[j] = !in ? 0.0f : s[j] == m ? 1.0f : expf(s[j] - m);
-                if (!in) ds[j] = 0.0f;
-                if (!a.o.renormalize) {
-                    ds[j] += dz[j];
-                    dz[j] = 0.0f;
-                }
-                part += s[j];
-                dot += ds[j] * s[j];
+        for (int j = 0; j < VPT; ++j) {
+            const bool in = s[j] > neg_inf();
+            s[j] = !in ? 0.0f : s[j] == m ? 1.0f : expf(s[j] - m);
+            if (!in) ds[j] = 0.0f;
+            if (!a.o.renormalize) {
+                ds[j] += dz[j];
+                dz[j] = 0.0f;
             }
-            const float inv = __fdividef(1.0f, warp_sum(part));
-            dot = warp_sum(dot) * inv;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (s[j] > 0.0f) dz[j] += s[j] * inv * (ds[j] - dot);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (s[j] > neg_inf()) {
-                    const float x = expf(-fabsf(s[j])), y = __fdividef(1.0f, 1.0f + x);
-                    dz[j] += ds[j] * x * y * y;
-                }
+            part += s[j];
+            dot += ds[j] * s[j];
         }
+        const float inv = __fdividef(1.0f, warp_sum(part));
+        dot = warp_sum(dot) * inv;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (s[j] > 0.0f) dz[j] += s[j] * inv * (ds[j] - dot);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (s[j] > neg_inf()) {
+                const float x = expf(-fabsf(s[j])), y = __fdividef(1.0f, 1.0f + x);
+                dz[j] += ds[j] * x * y * y;
+            }
     }
     float* out = a.dlogits + (size_t)t * E;
     if (VPT % 4 == 0 && vec) {
@@ -620,34 +717,131 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_kernel(const 
     }
 }
 
-template <int VPT, bool SOFTMAX, int WARPS>
+// Only the chosen logits matter (no dscores, and sigmoid or renormalised).
+// SLOTS lanes per token, 32 / SLOTS tokens per warp: their rows, which lie one
+// after the other, are put together in shared memory and leave as one run.
+template <int SLOTS>
+__global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_chosen_kernel(const __grid_constant__ RouteBwdArgs a) {
+    constexpr int TOK = 32 / SLOTS;
+    __shared__ __align__(16) float rows[kBwdWarps][TOK * kMaxExperts];
+    const int lane = threadIdx.x & 31, slot = lane & (SLOTS - 1);
+    const int t0 = (blockIdx.x * kBwdWarps + (threadIdx.x >> 5)) * TOK;
+    if (t0 >= a.T) return;  // warp-uniform
+    const int E = a.E, k = a.k, t = t0 + lane / SLOTS;
+    const bool softmax = a.o.softmax;
+    float* img = rows[threadIdx.x >> 5];
+    int e = -1;
+    float G = 0.0f, z = neg_inf();
+    if (slot < k && t < a.T) {
+        e = a.idx[(size_t)t * k + slot];
+        if (e < -1 || e >= E) {
+            report(a.status, kStDeviceCheck);
+            e = -1;
+        }
+        if (e >= 0) {
+            z = a.logits[(size_t)t * E + e];
+            G = a.dw[(size_t)t * k + slot] * a.o.scale;
+        }
+    }
+    const int count = min(TOK, a.T - t0) * E;
+    for (int i = 4 * lane; i < count; i += 128) *reinterpret_cast<float4*>(img + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool live = e >= 0 && z > neg_inf();  // not masked, not NaN
+    float c = 0.0f;
+    if (a.o.renormalize) {
+        const float p = chosen_share<SLOTS>(z, live, softmax);
+        float dot = live ? G * p : 0.0f;
+#pragma unroll
+        for (int o = SLOTS / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        if (live) c = p * (G - dot) * (softmax ? 1.0f : __fdividef(1.0f, 1.0f + expf(z)));
+    } else if (live) {
+        const float x = expf(-fabsf(z)), y = __fdividef(1.0f, 1.0f + x);
+        c = G * x * y * y;
+    }
+    // an expert listed twice: the first slot takes the sum, in slot order
+    const int at = lane / SLOTS * E + e;
+    const unsigned same = __match_any_sync(kFull, live ? at : -1 - lane);
+    bool first = live;
+    if (__any_sync(kFull, live && (same & (same - 1)) != 0)) {
+        float sum = 0.0f;
+        for (int r = 0; r < 32; ++r) {
+            const float x = __shfl_sync(kFull, c, r);
+            if ((same >> r) & 1u) sum += x;
+        }
+        if (live) c = sum;
+        first = live && __ffs(same) - 1 == lane;
+    }
+    __syncwarp();
+    if (first) img[at] = c;
+    __syncwarp();
+    float* out = a.dlogits + (size_t)t0 * E;
+    if ((TOK * E & 3) == 0) {  // every warp's run starts 16-byte aligned
+        for (int i = 4 * lane; i + 3 < count; i += 128)
+            *reinterpret_cast<float4*>(out + i) = *reinterpret_cast<const float4*>(img + i);
+        for (int i = (count & ~3) + lane; i < count; i += 32) out[i] = img[i];
+    } else {
+        for (int i = lane; i < count; i += 32) out[i] = img[i];
+    }
+}
+
+template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
 cudaError_t launch_route(const RouteArgs& a, int grid, cudaStream_t st) {
-    auto kern = route_logits_kernel<VPT, SOFTMAX, WARPS>;
+    auto kern = route_logits_kernel<VPT, SOFTMAX, WARPS, SMALL>;
     constexpr size_t smem = WARPS * sizeof(WarpMem) + kMaxExperts * sizeof(int);
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    kern<<<grid, WARPS * 32, smem, st>>>(a);
+    cudaLaunchAttribute attr[1];
+    if (SMALL) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)grid;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kern, a);
     note_launches(1);
-    return cudaGetLastError();
+    return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
 template <int VPT>
 cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
-    if (a.T <= 64)  // one CTA
-        return a.o.softmax ? launch_route<VPT, true, 32>(a, 1, st) : launch_route<VPT, false, 32>(a, 1, st);
-    const cudaError_t err = cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * (size_t)a.E, st);
+    constexpr int kSmallWarps = 16, kSmallCtas = 8;
+    if (a.T <= kSmallWarps * kSmallCtas) {  // a token per warp of one cluster
+        const int grid = a.T <= 8 ? 1 : kSmallCtas;
+        if (a.T <= 8 * kSmallCtas)
+            return a.o.softmax ? launch_route<VPT, true, 8, true>(a, grid, st)
+                               : launch_route<VPT, false, 8, true>(a, grid, st);
+        return a.o.softmax ? launch_route<VPT, true, kSmallWarps, true>(a, grid, st)
+                           : launch_route<VPT, false, kSmallWarps, true>(a, grid, st);
+    }
+    clear_counts_kernel<<<1, 256, 0, st>>>(a.counts, a.E);
+    note_launches(1);
+    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const int blocks = (a.T + 7) / 8, grid = blocks < 4 * num_sms ? blocks : 4 * num_sms;
-    return a.o.softmax ? launch_route<VPT, true, 8>(a, grid, st) : launch_route<VPT, false, 8>(a, grid, st);
+    return a.o.softmax ? launch_route<VPT, true, 8, false>(a, grid, st) : launch_route<VPT, false, 8, false>(a, grid, st);
 }
 
 template <int VPT>
 cudaError_t launch_bwd_v(const RouteBwdArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kBwdWarps - 1) / kBwdWarps);
-    if (a.dscores || (a.o.softmax && !a.o.renormalize))
-        route_logits_bwd_kernel<VPT, true><<<grid, kBwdWarps * 32, 0, st>>>(a);
-    else
-        route_logits_bwd_kernel<VPT, false><<<grid, kBwdWarps * 32, 0, st>>>(a);
+    route_logits_bwd_kernel<VPT><<<grid, kBwdWarps * 32, 0, st>>>(a);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+template <int SLOTS>
+cudaError_t launch_bwd_chosen(const RouteBwdArgs& a, cudaStream_t st) {
+    constexpr int per_cta = kBwdWarps * 32 / SLOTS;
+    route_logits_bwd_chosen_kernel<SLOTS><<<(unsigned)((a.T + per_cta - 1) / per_cta), kBwdWarps * 32, 0, st>>>(a);
     note_launches(1);
     return cudaGetLastError();
 }
@@ -657,12 +851,21 @@ cudaError_t launch_bwd_v(const RouteBwdArgs& a, cudaStream_t st) {
 cudaError_t launch_route_logits(const float* logits, const float* bias, int T, int E, int k, const RouteOpts& o,
                                 int32_t* idx, float* w, int32_t* counts, int* status, int num_sms, cudaStream_t st) {
     if (T == 0) return cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)E, st);
-    const int per = E / o.groups;
-    const RouteArgs a{logits, bias, T, E, k, (65536 + per - 1) / per, o, idx, w, counts, status};
-    return E <= 32    ? launch_route_v<1>(a, num_sms, st)
-           : E <= 64  ? launch_route_v<2>(a, num_sms, st)
-           : E <= 128 ? launch_route_v<4>(a, num_sms, st)
-                      : launch_route_v<8>(a, num_sms, st);
+    const int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
+    const int per = E / o.groups, whole = per % vpt == 0 ? per / vpt : 0;
+    int lanes = whole > 0 && (whole & (whole - 1)) == 0 ? whole : 1;
+    if (whole != lanes)
+        while (2 * lanes * o.groups <= 32) lanes *= 2;
+    unsigned leaders = 0u;
+    for (int g = 0; g < o.groups; ++g) leaders |= 1u << (g * lanes);
+    const RouteArgs a{logits, bias, T,      E,      k, per, (65536 + per - 1) / per, lanes, leaders, o, idx, w,
+                      counts, status};
+    switch (vpt) {
+        case 1: return launch_route_v<1>(a, num_sms, st);
+        case 2: return launch_route_v<2>(a, num_sms, st);
+        case 4: return launch_route_v<4>(a, num_sms, st);
+        default: return launch_route_v<8>(a, num_sms, st);
+    }
 }
 
 cudaError_t launch_route_logits_bwd(const float* logits, const int32_t* idx, const float* dw, const float* dscores,
@@ -670,6 +873,8 @@ cudaError_t launch_route_logits_bwd(const float* logits, const int32_t* idx, con
                                     cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     const RouteBwdArgs a{logits, idx, dw, dscores, T, E, k, o, dlogits, status};
+    if (!dscores && (!o.softmax || o.renormalize))
+        return k <= 8 ? launch_bwd_chosen<8>(a, st) : launch_bwd_chosen<16>(a, st);
     return E <= 32    ? launch_bwd_v<1>(a, st)
            : E <= 64  ? launch_bwd_v<2>(a, st)
            : E <= 128 ? launch_bwd_v<4>(a, st)
