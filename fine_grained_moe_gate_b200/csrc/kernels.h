@@ -71,7 +71,7 @@ cudaError_t launch_router_tc(const void* x, const void* wg, const float* bias, i
                              int32_t* idx, float* w, int32_t* counts, float* aff, int* status, int num_sms,
                              cudaStream_t st);
 
-// Gate logits z = x W_g^T, fp32 [T][E]: router_tc.cu (bf16, tensor cores), router.cu (fp32)
+// Gate logits z = x W_g^T, fp32 [T][E]: gate_logits.cu (bf16, tensor cores), router.cu (fp32)
 cudaError_t launch_gate_logits_tc(const void* x, const void* wg, int T, int d, int E, float* logits, int* status,
                                   int num_sms, cudaStream_t st);
 cudaError_t launch_gate_logits_simt(const float* x, const float* wg, int T, int d, int E, float* logits,

@@ -74,20 +74,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
     return v;
 }
 
-// Up to 16 consecutive logits of a token (n of them lie inside the row).
-__device__ __forceinline__ void store_logits16(float* dst, const uint32_t (&v)[16], int n, bool vec) {
-    if (vec) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (4 * i < n)
-                reinterpret_cast<uint4*>(dst)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < n) dst[i] = __uint_as_float(v[i]);
-    }
-}
-
 // Split K: the C CTAs (or CTA pairs) of a cluster share one token tile, CTA
 // (pair) c running the MMA over its slice of d; the slices' fp32 partial
 // scores are summed in the fixed order c = 0..C-1 through distributed shared
@@ -97,9 +83,7 @@ __device__ __forceinline__ void store_logits16(float* dst, const uint32_t (&v)[1
 // is the plain tile.  PAIR: a cluster of 2C CTAs, ranks 2c and 2c + 1 forming
 // the pair of slice c; the even CTA issues the MMAs, the odd one holds tokens
 // 128..255 of the tile and W_gate rows [N/2, N).
-// RAW: only the gate product leaves, `aff` receives the logits z (no sigmoid);
-// bias, idx, w and counts are not touched.
-template <int KMAX, int C, bool PAIR, bool RAW = false>
+template <int KMAX, int C, bool PAIR>
 __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
     router_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const float* __restrict__ bias, int T, int E, int n_pad, uint32_t tmem_cols, int k_blocks,
@@ -129,11 +113,10 @@ __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
     const int kb0 = slice * k_blocks / C, kb1 = (slice + 1) * k_blocks / C;
     const int n_rows = PAIR ? n_pad / 2 : n_pad;  // W_gate rows this CTA loads per stage
 
-    if (!RAW)
-        for (int e = tid; e < E; e += NTHREADS) {
-            ctl->bias[e] = bias[e];
-            ctl->hist[e] = 0;
-        }
+    for (int e = tid; e < E; e += NTHREADS) {
+        ctl->bias[e] = bias[e];
+        ctl->hist[e] = 0;
+    }
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&ctl->full[s], 1);
@@ -261,18 +244,7 @@ __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
         const int q = warp & 3;
         const int r = q * 32 + lane;
         const int t = t0 + r;
-        if (RAW) {
-            if (mbar_wait(&ctl->tfull, 0, &ctl->abort, status)) {
-                tc_fence_after();
-                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
-                for (int c = 0; c < n_pad; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(taddr + (uint32_t)c, v);
-                    tmem_ld_wait();
-                    if (t < T) store_logits16(aff + (size_t)t * E + c, v, E - c, (E & 3) == 0);
-                }
-            }
-        } else if (mbar_wait(&ctl->tfull, 0, &ctl->abort, status)) {
+        if (mbar_wait(&ctl->tfull, 0, &ctl->abort, status)) {
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
             TopK<KMAX> tk;
@@ -375,104 +347,90 @@ __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
                     z.w = __fadd_rn(z.w, o.w);
                 }
                 const float zs[4] = {z.x, z.y, z.z, z.w};
-                if (RAW) {
-                    float* dst = aff + (size_t)(t0 + r) * E + e;
-                    if (keep_aff && (E & 3) == 0) {
-                        *reinterpret_cast<float4*>(dst) = z;
-                    } else if (keep_aff) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (e + i < E) dst[i] = zs[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (e + i < E) {
-                            const float s = sigmoid_f32(zs[i]);
-                            sc[rl * PS + e + i] = s;
-                            if (keep_aff) aff[(size_t)(t0 + r) * E + e + i] = s;
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    if (e + i < E) {
+                        const float s = sigmoid_f32(zs[i]);
+                        sc[rl * PS + e + i] = s;
+                        if (keep_aff) aff[(size_t)(t0 + r) * E + e + i] = s;
                     }
                 }
             }
         }
-        if (!RAW) {
-            __syncthreads();
-            // top-k: P threads per token, thread `sub` takes experts sub, sub + P, ...
-            const int rl = u / P, sub = u - rl * P;
-            const int t = t0 + tl0 + rl;
-            TopK<KMAX> tk;
-            tk.init();
-            if (P >= k && E <= 32 * P) {
-                // The P threads' largest v are P >= k distinct experts, so the k-th
-                // largest v of the token is at least their minimum: experts below it
-                // cannot be chosen.  Each thread marks its experts at or above it in a
-                // bit mask and pushes only those, in expert order; without the mask
-                // the warp ran the insertion for every expert that any lane inserted.
-                float vmax = -FLT_MAX;
-                for (int e = sub; e < E; e += P) vmax = fmaxf(vmax, __fadd_rn(sc[rl * PS + e], ctl->bias[e]));
-                float th = vmax;
-    #pragma unroll
-                for (int o = P / 2; o > 0; o >>= 1) th = fminf(th, __shfl_xor_sync(0xffffffffu, th, o));
-                uint32_t mask = 0u;
-                for (int e = sub, j = 0; e < E; e += P, ++j)
-                    if (__fadd_rn(sc[rl * PS + e], ctl->bias[e]) >= th) mask |= 1u << j;
-                while (mask) {
-                    const int e = sub + (__ffs(mask) - 1) * P;
-                    mask &= mask - 1u;
-                    const float s = sc[rl * PS + e];
-                    tk.push(__fadd_rn(s, ctl->bias[e]), s, e);
-                }
-            } else {
-                for (int e = sub; e < E; e += P) {
-                    const float s = sc[rl * PS + e];
-                    tk.push(__fadd_rn(s, ctl->bias[e]), s, e);
-                }
+        __syncthreads();
+        // top-k: P threads per token, thread `sub` takes experts sub, sub + P, ...
+        const int rl = u / P, sub = u - rl * P;
+        const int t = t0 + tl0 + rl;
+        TopK<KMAX> tk;
+        tk.init();
+        if (P >= k && E <= 32 * P) {
+            // The P threads' largest v are P >= k distinct experts, so the k-th
+            // largest v of the token is at least their minimum: experts below it
+            // cannot be chosen.  Each thread marks its experts at or above it in a
+            // bit mask and pushes only those, in expert order; without the mask
+            // the warp ran the insertion for every expert that any lane inserted.
+            float vmax = -FLT_MAX;
+            for (int e = sub; e < E; e += P) vmax = fmaxf(vmax, __fadd_rn(sc[rl * PS + e], ctl->bias[e]));
+            float th = vmax;
+#pragma unroll
+            for (int o = P / 2; o > 0; o >>= 1) th = fminf(th, __shfl_xor_sync(0xffffffffu, th, o));
+            uint32_t mask = 0u;
+            for (int e = sub, j = 0; e < E; e += P, ++j)
+                if (__fadd_rn(sc[rl * PS + e], ctl->bias[e]) >= th) mask |= 1u << j;
+            while (mask) {
+                const int e = sub + (__ffs(mask) - 1) * P;
+                mask &= mask - 1u;
+                const float s = sc[rl * PS + e];
+                tk.push(__fadd_rn(s, ctl->bias[e]), s, e);
             }
-            {  // merge the P lists in (v desc, index asc) order
-                TopK<KMAX> m;
-                m.init();
-                int pos = 0;
-    #pragma unroll
-                for (int j = 0; j < KMAX; ++j) {
-                    float hv = -FLT_MAX, hs = 0.f;
-                    int hid = 0x7fffffff;
-    #pragma unroll
-                    for (int i = 0; i < KMAX; ++i)
-                        if (i == pos && tk.id[i] >= 0) {
-                            hv = tk.v[i];
-                            hs = tk.s[i];
-                            hid = tk.id[i];
-                        }
-                    float bv = hv, bs = hs;
-                    int bid = hid;
-    #pragma unroll
-                    for (int o = P / 2; o > 0; o >>= 1) {
-                        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-                        const float os = __shfl_xor_sync(0xffffffffu, bs, o);
-                        const int oid = __shfl_xor_sync(0xffffffffu, bid, o);
-                        if (ov > bv || (ov == bv && oid < bid)) {
-                            bv = ov;
-                            bs = os;
-                            bid = oid;
-                        }
-                    }
-                    if (bid != 0x7fffffff) {
-                        m.v[j] = bv;
-                        m.s[j] = bs;
-                        m.id[j] = bid;
-                        if (bid == hid) ++pos;
-                    }
-                }
-                tk = m;
+        } else {
+            for (int e = sub; e < E; e += P) {
+                const float s = sc[rl * PS + e];
+                tk.push(__fadd_rn(s, ctl->bias[e]), s, e);
             }
-            if (sub == 0 && t < T) emit_route<KMAX>(tk, k, idx + (size_t)t * k, w + (size_t)t * k, ctl->hist, status);
         }
+        {  // merge the P lists in (v desc, index asc) order
+            TopK<KMAX> m;
+            m.init();
+            int pos = 0;
+#pragma unroll
+            for (int j = 0; j < KMAX; ++j) {
+                float hv = -FLT_MAX, hs = 0.f;
+                int hid = 0x7fffffff;
+#pragma unroll
+                for (int i = 0; i < KMAX; ++i)
+                    if (i == pos && tk.id[i] >= 0) {
+                        hv = tk.v[i];
+                        hs = tk.s[i];
+                        hid = tk.id[i];
+                    }
+                float bv = hv, bs = hs;
+                int bid = hid;
+#pragma unroll
+                for (int o = P / 2; o > 0; o >>= 1) {
+                    const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
+                    const float os = __shfl_xor_sync(0xffffffffu, bs, o);
+                    const int oid = __shfl_xor_sync(0xffffffffu, bid, o);
+                    if (ov > bv || (ov == bv && oid < bid)) {
+                        bv = ov;
+                        bs = os;
+                        bid = oid;
+                    }
+                }
+                if (bid != 0x7fffffff) {
+                    m.v[j] = bv;
+                    m.s[j] = bs;
+                    m.id[j] = bid;
+                    if (bid == hid) ++pos;
+                }
+            }
+            tk = m;
+        }
+        if (sub == 0 && t < T) emit_route<KMAX>(tk, k, idx + (size_t)t * k, w + (size_t)t * k, ctl->hist, status);
     }
     __syncthreads();
-    if (!RAW)
-        for (int e = tid; e < E; e += NTHREADS)
-            if (ctl->hist[e]) atomicAdd(&counts[e], ctl->hist[e]);
+    for (int e = tid; e < E; e += NTHREADS)
+        if (ctl->hist[e]) atomicAdd(&counts[e], ctl->hist[e]);
     // no CTA leaves while its partial scores may still be read, or while its
     // pair leader's MMAs may still read its shared memory
     if (CL > 1) cluster_sync_all();
@@ -485,11 +443,11 @@ __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
     }
 }
 
-template <int KMAX, int C, bool PAIR, bool RAW>
+template <int KMAX, int C, bool PAIR>
 cudaError_t launch_kc(const CUtensorMap& tx, const CUtensorMap& tw, const float* bias, int T, int E, int n_pad,
                       uint32_t cols, int kb, int k, int32_t* idx, float* w, int32_t* counts, float* aff, int* status,
                       cudaStream_t st) {
-    auto kern = router_tc_kernel<KMAX, C, PAIR, RAW>;
+    auto kern = router_tc_kernel<KMAX, C, PAIR>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (err != cudaSuccess) return err;
     constexpr int CL = PAIR ? 2 * C : C;
@@ -511,51 +469,21 @@ cudaError_t launch_kc(const CUtensorMap& tx, const CUtensorMap& tw, const float*
     return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
-template <int KMAX, bool PAIR, bool RAW = false>
+template <int KMAX, bool PAIR>
 cudaError_t launch_k(const CUtensorMap& tx, const CUtensorMap& tw, const float* bias, int T, int E, int n_pad,
                      uint32_t cols, int kb, int k, int32_t* idx, float* w, int32_t* counts, float* aff, int* status,
                      int split, cudaStream_t st) {
     switch (split) {
         case 8:
             if (!PAIR)  // a pair cluster of 16 CTAs is not portable
-                return launch_kc<KMAX, 8, false, RAW>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status,
+                return launch_kc<KMAX, 8, false>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status,
                                                  st);
             return cudaErrorInvalidValue;
-        case 4: return launch_kc<KMAX, 4, PAIR, RAW>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, st);
-        case 2: return launch_kc<KMAX, 2, PAIR, RAW>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, st);
+        case 4: return launch_kc<KMAX, 4, PAIR>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, st);
+        case 2: return launch_kc<KMAX, 2, PAIR>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, st);
         default:
-            return launch_kc<KMAX, 1, PAIR, RAW>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, st);
+            return launch_kc<KMAX, 1, PAIR>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, st);
     }
-}
-
-// How a T x d gate product over E experts is launched.
-struct Plan {
-    CUtensorMap tx, tw;
-    int n_pad, kb, split;
-    uint32_t cols;
-    bool pair;
-};
-bool make_plan(const void* x, const void* wg, int T, int d, int E, int num_sms, Plan* o) {
-    if (d % BK != 0 || E > kMaxExperts || E <= 0) return false;
-    const int n_pad = (E + 15) / 16 * 16;  // MMA N: a multiple of 16 (N/2 rows per CTA of a pair: 8-row atoms)
-    uint32_t cols = 32;
-    while (cols < (uint32_t)n_pad) cols <<= 1;  // TMEM allocation: power of two >= 32
-    // Large batches: CTA pairs of 256 tokens (half the W_gate rows per CTA);
-    // the one-CTA form only while its K split would still reach 4 or more.
-    const int tiles1 = (T + BM - 1) / BM, kb = d / BK;
-    const bool pair = T > 2 * BM && tiles1 * 4 > num_sms;
-    if (!make_tmap_2d(&o->tx, x, d, T, d, BK, BM) || !make_tmap_2d(&o->tw, wg, d, E, d, BK, pair ? n_pad / 2 : n_pad))
-        return false;
-    // K split: as many CTAs per token tile as keep the grid within one wave of SMs
-    const int tiles = pair ? (T + 2 * BM - 1) / (2 * BM) : tiles1, per = pair ? 2 : 1;
-    int split = pair ? 4 : 8;  // clusters of at most 8 CTAs
-    while (split > 1 && (tiles * split * per > num_sms || split > kb)) split >>= 1;
-    o->n_pad = n_pad;
-    o->kb = kb;
-    o->split = split;
-    o->cols = cols;
-    o->pair = pair;
-    return true;
 }
 
 }  // namespace
@@ -564,29 +492,27 @@ cudaError_t launch_router_tc(const void* x, const void* wg, const float* bias, i
                              int32_t* idx, float* w, int32_t* counts, float* aff, int* status, int num_sms,
                              cudaStream_t st) {
     if (T == 0) return cudaSuccess;
-    Plan p;
-    if (!make_plan(x, wg, T, d, E, num_sms, &p)) return cudaErrorInvalidValue;
-    if (p.pair)
-        return k <= 8 ? launch_k<8, true>(p.tx, p.tw, bias, T, E, p.n_pad, p.cols, p.kb, k, idx, w, counts, aff, status,
-                                          p.split, st)
-                      : launch_k<16, true>(p.tx, p.tw, bias, T, E, p.n_pad, p.cols, p.kb, k, idx, w, counts, aff,
-                                           status, p.split, st);
-    return k <= 8 ? launch_k<8, false>(p.tx, p.tw, bias, T, E, p.n_pad, p.cols, p.kb, k, idx, w, counts, aff, status,
-                                       p.split, st)
-                  : launch_k<16, false>(p.tx, p.tw, bias, T, E, p.n_pad, p.cols, p.kb, k, idx, w, counts, aff, status,
-                                        p.split, st);
-}
-
-cudaError_t launch_gate_logits_tc(const void* x, const void* wg, int T, int d, int E, float* logits, int* status,
-                                  int num_sms, cudaStream_t st) {
-    if (T == 0) return cudaSuccess;
-    Plan p;
-    if (!make_plan(x, wg, T, d, E, num_sms, &p)) return cudaErrorInvalidValue;
-    if (p.pair)
-        return launch_k<8, true, true>(p.tx, p.tw, nullptr, T, E, p.n_pad, p.cols, p.kb, 1, nullptr, nullptr, nullptr,
-                                       logits, status, p.split, st);
-    return launch_k<8, false, true>(p.tx, p.tw, nullptr, T, E, p.n_pad, p.cols, p.kb, 1, nullptr, nullptr, nullptr,
-                                    logits, status, p.split, st);
+    if (d % BK != 0 || E > kMaxExperts || E <= 0) return cudaErrorInvalidValue;
+    const int n_pad = (E + 15) / 16 * 16;  // MMA N: a multiple of 16 (N/2 rows per CTA of a pair: 8-row atoms)
+    uint32_t cols = 32;
+    while (cols < (uint32_t)n_pad) cols <<= 1;  // TMEM allocation: power of two >= 32
+    // Large batches: CTA pairs of 256 tokens (half the W_gate rows per CTA);
+    // the one-CTA form only while its K split would still reach 4 or more.
+    const int tiles1 = (T + BM - 1) / BM, kb = d / BK;
+    const bool pair = T > 2 * BM && tiles1 * 4 > num_sms;
+    CUtensorMap tx, tw;
+    if (!make_tmap_2d(&tx, x, d, T, d, BK, BM) || !make_tmap_2d(&tw, wg, d, E, d, BK, pair ? n_pad / 2 : n_pad))
+        return cudaErrorInvalidValue;
+    // K split: as many CTAs per token tile as keep the grid within one wave of SMs
+    const int tiles = pair ? (T + 2 * BM - 1) / (2 * BM) : tiles1, per = pair ? 2 : 1;
+    int split = pair ? 4 : 8;  // clusters of at most 8 CTAs
+    while (split > 1 && (tiles * split * per > num_sms || split > kb)) split >>= 1;
+    if (pair)
+        return k <= 8 ? launch_k<8, true>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, split, st)
+                      : launch_k<16, true>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, split,
+                                           st);
+    return k <= 8 ? launch_k<8, false>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, split, st)
+                  : launch_k<16, false>(tx, tw, bias, T, E, n_pad, cols, kb, k, idx, w, counts, aff, status, split, st);
 }
 
 }  // namespace moe
