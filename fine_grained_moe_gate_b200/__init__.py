@@ -41,6 +41,7 @@ EXPORTS = (
     "moe_layer_backward", "moe_backward_workspace_size",
     "moe_gate_logits", "moe_route_logits", "moe_route_logits_backward", "moe_ffn_up_save",
     "moe_swiglu_backward_saved",
+    "moe_layer_forward_logits", "moe_layer_backward_logits", "moe_backward_logits_workspace_size",
 )
 
 MOE_ROUTED, MOE_SHARED = 0, 1
@@ -155,6 +156,10 @@ def lib() -> ctypes.CDLL:
             "moe_route_logits_backward": [P, P, P, P, S, MoERouteOpts, P, P],
             "moe_ffn_up_save": [P, P, P, P, P, P, P, S, P, P, ctypes.POINTER(MoESavedActs), P],
             "moe_swiglu_backward_saved": [ctypes.POINTER(MoESavedActs), S, ctypes.c_int32, P, P, P, P, P, P, P],
+            "moe_layer_forward_logits": [P, P, P, P, P, P, P, P, P, S, MoERouteOpts, P, P, P, P, P,
+                                         ctypes.POINTER(MoESavedActs), P, sz, P],
+            "moe_layer_backward_logits": [P, P, P, P, P, P, P, P, S, MoERouteOpts, ctypes.POINTER(MoESavedActs), P, P,
+                                          P, P, P, P, F, ctypes.c_int32, P, P, P, P, P, P, P, P, P, P, sz, P],
             "moe_layer_backward": [P, P, P, P, P, P, P, P, S, P, P, P, P, P, F, ctypes.c_int32, P, P, P, P, P, P, P,
                                    P, P, P, sz, P],
         }
@@ -168,6 +173,8 @@ def lib() -> ctypes.CDLL:
             fn.restype = sz
         L.moe_backward_workspace_size.argtypes = [S, ctypes.c_int32]
         L.moe_backward_workspace_size.restype = sz
+        L.moe_backward_logits_workspace_size.argtypes = [S, ctypes.c_int32, ctypes.c_int32]
+        L.moe_backward_logits_workspace_size.restype = sz
         L.moe_fp8_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
         L.moe_fp8_scale_bytes.restype = sz
         L.moe_fp8_tile_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
@@ -468,6 +475,31 @@ def moe_ffn_up_save(x_perm, offsets, w1, w3, x, ws1, ws3, shape, h, hs, saved, s
 def moe_swiglu_backward_saved(saved, shape, expert_set, u, perm_tok, topk_w, dadg, h, dw, stream=None):
     _check(lib().moe_swiglu_backward_saved(ctypes.byref(saved), shape, expert_set, _p(u), _p(perm_tok), _p(topk_w),
                                            _p(dadg), _p(h), _p(dw), _stream(stream)), "moe_swiglu_backward_saved")
+
+
+# ---- the layer with routing from logits ------------------------------------------
+
+def moe_layer_forward_logits(x, w_gate, bias, w1, w3, w2, ws1, ws3, ws2, shape, opts, y, logits, topk_idx, topk_w,
+                             counts, saved, workspace, stream=None):
+    _check(lib().moe_layer_forward_logits(_p(x), _p(w_gate), _p(bias), _p(w1), _p(w3), _p(w2), _p(ws1), _p(ws3),
+                                          _p(ws2), shape, opts, _p(y), _p(logits), _p(topk_idx), _p(topk_w),
+                                          _p(counts), None if saved is None else ctypes.byref(saved), _p(workspace),
+                                          _nbytes(workspace), _stream(stream)), "moe_layer_forward_logits")
+
+
+def moe_backward_logits_workspace_size(shape, seq_len: int = 0, saved: bool = False) -> int:
+    return lib().moe_backward_logits_workspace_size(shape, int(seq_len), int(bool(saved)))
+
+
+def moe_layer_backward_logits(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape, opts, saved, logits, topk_idx, topk_w,
+                              counts, dscores, dy, alpha, seq_len, dx, dw_gate, dw1, dw3, dw2, dws1, dws3, dws2,
+                              balance_loss, workspace, stream=None):
+    _check(lib().moe_layer_backward_logits(_p(x), _p(w_gate), _p(w1), _p(w3), _p(w2), _p(ws1), _p(ws3), _p(ws2),
+                                           shape, opts, None if saved is None else ctypes.byref(saved), _p(logits),
+                                           _p(topk_idx), _p(topk_w), _p(counts), _p(dscores), _p(dy), float(alpha),
+                                           int(seq_len), _p(dx), _p(dw_gate), _p(dw1), _p(dw3), _p(dw2), _p(dws1),
+                                           _p(dws3), _p(dws2), _p(balance_loss), _p(workspace), _nbytes(workspace),
+                                           _stream(stream)), "moe_layer_backward_logits")
 
 
 # ---- expert parallelism --------------------------------------------------------

@@ -69,6 +69,10 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_bwd_saved_kernel(const __g
     if (r >= p.rows) return;  // warp-uniform
     const int n = p.n;
     const long long pr = p.prow ? p.prow[r] : r;
+    if (p.prow && (pr < 0 || pr >= p.prow_rows)) {  // warp-uniform
+        if (lane == 0) report(p.status, kStDeviceCheck);
+        return;
+    }
     float wt = 1.0f;
     long long q = r;
     if (p.perm) {
@@ -130,8 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_bwd_saved_kernel(const __g
 
 }  // namespace
 
-cudaError_t launch_swiglu_bwd_saved(const SwigluBwdSaved& p, int num_sms, cudaStream_t st) {
-    (void)num_sms;
+cudaError_t launch_swiglu_bwd_saved(const SwigluBwdSaved& p, cudaStream_t st) {
     if (p.rows <= 0) return cudaSuccess;
     const long long blocks = (p.rows + kWarps - 1) / kWarps;
     swiglu_bwd_saved_kernel<4><<<(unsigned)blocks, kWarps * 32, 0, st>>>(p);

@@ -450,6 +450,52 @@ __global__ void router_bwd_kernel(const float* __restrict__ s, const int32_t* __
     }
 }
 
+// Routing from logits, one warp per token: the scores s (sigmoid or softmax;
+// masked logits 0) and tot[t] = sum_i s_ti for the balance loss, and the
+// upstream gradient of s: dscores (if any) plus the balance term.
+__global__ void scores_kernel(const float* __restrict__ logits, const float* __restrict__ dscores,
+                              const int32_t* __restrict__ cnt, float alpha, int L, int nb, int T, int E, int k,
+                              int softmax, float* __restrict__ s, float* __restrict__ tot, float* __restrict__ ds) {
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * warps + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const float* z = logits + (long long)t * E;
+    float* st = s + (long long)t * E;
+    const float ninf = __int_as_float(0xff800000);
+    float m = ninf, den = 0.0f;
+    if (softmax) {
+        for (int i = lane; i < E; i += 32) m = fmaxf(m, z[i]);  // NaN drops out
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int i = lane; i < E; i += 32)
+            if (z[i] > ninf) den += z[i] == m ? 1.0f : expf(z[i] - m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    }
+    const float fscale = (float)E / ((float)k * (float)L);
+    const int32_t* cb = cnt + (long long)(t / L) * E;
+    float sum_s = 0.0f, sum_fs = 0.0f;
+    for (int i = lane; i < E; i += 32) {
+        const float zi = z[i];
+        const float v = !(zi > ninf) ? 0.0f : softmax ? (zi == m ? 1.0f : expf(zi - m)) / den : sigmoid_acc(zi);
+        st[i] = v;
+        sum_s += v;
+        sum_fs += fscale * (float)cb[i] * v;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum_s += __shfl_xor_sync(0xffffffffu, sum_s, o);
+        sum_fs += __shfl_xor_sync(0xffffffffu, sum_fs, o);
+    }
+    if (!(sum_s > 0.0f)) sum_s = 1.0f;  // every expert masked: no scores, no gradient
+    if (lane == 0) tot[t] = sum_s;
+    const float c = alpha / ((float)nb * (float)L) / sum_s;
+    for (int i = lane; i < E; i += 32) {
+        const float d = dscores ? dscores[(long long)t * E + i] : 0.0f;
+        ds[(long long)t * E + i] = d + c * (fscale * (float)cb[i] - sum_fs / sum_s);
+    }
+}
+
 constexpr int kLossChunk = 32;  // tokens per partial sum of the balance loss
 
 // Block (c, b): chunk[b][c][i] = sum over tokens t of chunk c of sequence b of s_ti / tot_t.  The block's
@@ -569,12 +615,14 @@ __device__ __forceinline__ int last_le(const int32_t* a, int n, int v) {
 }
 
 // One warp per permuted row r: prow[r] = its padded row; x_pad[prow[r]] = x[perm[r] / k] (bf16, 16-byte copies).
+// Rows past offsets[E] (assignments to no expert) are left alone.
 __global__ void gather_pad_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ perm,
                                   const int32_t* __restrict__ offsets, const int32_t* __restrict__ pstart, int E,
                                   int k, int R, int T, int vec, int32_t* __restrict__ prow, uint4* __restrict__ xp,
                                   int* status) {
     const int lane = threadIdx.x & 31;
-    for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < R; r += gridDim.x * (blockDim.x >> 5)) {
+    const int rows = min(R, offsets[E]);
+    for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += gridDim.x * (blockDim.x >> 5)) {
         const int e = last_le(offsets, E, r);
         const int pr = pstart[e] + (r - offsets[e]);
         const int t = perm[r] / k;
@@ -640,6 +688,7 @@ __global__ void __launch_bounds__(256) swiglu_bwd_dw_pad_kernel(const float* __r
     if (r >= R) return;  // warp-uniform
     const long long pr = prow[r];
     const int q = perm[r];
+    if (pr < 0 || q < 0) return;  // no assignment (routing from logits); warp-uniform
     const float wq = w[q];
     const int n4 = n / 4;
     const float4* ar = reinterpret_cast<const float4*>(a + pr * n);
@@ -800,6 +849,8 @@ struct BwdCarve {
 // Buffers of the backward, carved from the workspace in this order (the
 // sizes depend on the path: fp32 SIMT, or the tensor cores' padded bf16 layout).
 struct BwdBufs {
+    // routing from logits with a balance loss: the scores and their gradient
+    float *scores, *dscores;
     int32_t *offsets, *perm, *inv, *pscratch, *cnt;
     float *dw, *dz, *tot, *part, *chunk;
     // SIMT path
@@ -810,7 +861,8 @@ struct BwdBufs {
     float *a_pad, *g_pad, *o_pad, *dh_pad, *as32, *gs32, *dhs32;
 };
 
-size_t carve(BwdBufs* o, char* base, int T, int d, int E, int k, int I, int S, int Is, int seq_len, bool tc) {
+size_t carve(BwdBufs* o, char* base, int T, int d, int E, int k, int I, int S, int Is, int seq_len, bool tc,
+             bool logits = false, bool saved = false) {
     BwdCarve c{base};
     const size_t R = (size_t)T * k;
     const size_t nb = seq_len > 0 ? (size_t)T / seq_len : 0;
@@ -845,25 +897,31 @@ size_t carve(BwdBufs* o, char* base, int T, int d, int E, int k, int I, int S, i
         b.h_pad = c.take<uint16_t>(Rp * I * 2);
         b.do_pad = c.take<uint16_t>(Rp * d * 2);
         b.dadg = c.take<uint16_t>(Rp * 2 * I * 2);
-        b.a_pad = c.take<float>(Rp * I * 4);
-        b.g_pad = c.take<float>(Rp * I * 4);
+        b.a_pad = c.take<float>(saved ? 0 : Rp * I * 4);
+        b.g_pad = c.take<float>(saved ? 0 : Rp * I * 4);
         b.dh_pad = c.take<float>(Rp * I * 4);
         b.o_pad = c.take<float>(Rp * d * 4);
-        b.as32 = c.take<float>((size_t)T * SI * 4);
-        b.gs32 = c.take<float>((size_t)T * SI * 4);
+        b.as32 = c.take<float>(saved ? 0 : (size_t)T * SI * 4);
+        b.gs32 = c.take<float>(saved ? 0 : (size_t)T * SI * 4);
         b.dhs32 = c.take<float>((size_t)T * SI * 4);
         b.hs16 = c.take<uint16_t>((size_t)T * SI * 2);
         b.dys16 = c.take<uint16_t>((size_t)T * d * 2);
         b.dadgs = c.take<uint16_t>((size_t)T * 2 * SI * 2);
         b.dz16 = c.take<uint16_t>((size_t)T * E * 2);
     }
+    if (logits) {
+        b.scores = c.take<float>(nb ? (size_t)T * E * 4 : 0);
+        b.dscores = c.take<float>(nb ? (size_t)T * E * 4 : 0);
+    }
     if (o) *o = b;
     return c.used;
 }
 }  // namespace
 
-size_t backward_scratch_bytes(int T, int d, int E, int k, int I, int S, int Is, int seq_len, bool bf16) {
-    return carve(nullptr, nullptr, T, d, E, k, I, S, Is, seq_len, backward_on_tensor_cores(bf16, d, I, S, Is));
+size_t backward_scratch_bytes(int T, int d, int E, int k, int I, int S, int Is, int seq_len, bool bf16, bool logits,
+                              bool saved) {
+    return carve(nullptr, nullptr, T, d, E, k, I, S, Is, seq_len, backward_on_tensor_cores(bf16, d, I, S, Is), logits,
+                 saved);
 }
 
 namespace {
@@ -942,7 +1000,9 @@ cudaError_t experts_backward_tc(const BackwardArgs& a, const BwdBufs& b, int* st
     // ---- recompute, routed and shared experts in one launch of the forward's gate/up GEMM: a = x W1^T and
     // g = x W3^T (fp32) beside h = bf16(silu(a) g), the very h the forward computed.  The routed groups are the
     // padded segments (pstart), whose zero padding rows give a = g = h = 0; the shared set is one group of T rows.
-    {
+    // With a and g saved by the forward, h comes from them in the SwiGLU backward, before it is first read.
+    const bool saved = a.saved_routed != nullptr;
+    if (!saved) {
         TcUpArgs ur{};
         ur.A = b.x_pad;
         ur.A_rows = Rp;
@@ -985,14 +1045,30 @@ cudaError_t experts_backward_tc(const BackwardArgs& a, const BwdBufs& b, int* st
         note_launches(1);
     }
     // dW2_e = do^T h
-    TC_TRY(launch_bwd_wgrad(wgrad_args(b.do_pad, d, 0, b.h_pad, I, 0, Rp, d, I, a.dw2, true), status, num_sms, st));
+    const auto dw2 = [&] {
+        return launch_bwd_wgrad(wgrad_args(b.do_pad, d, 0, b.h_pad, I, 0, Rp, d, I, a.dw2, true), status, num_sms, st);
+    };
+    if (!saved) TC_TRY(dw2());
     // u = dy W2_e (W2 read along its output dimension); dh = w u.  The combine weight's gradient
     // <dy_t, o> = <dy_t, W2_e h> = <u, h> comes with it, so o is never recomputed.
     {
         BwdRowsArgs r = rows_args(a.w2, (long long)E * d, d, dy_pad, Rp, d, I, b.dh_pad, true);
         TC_TRY(launch_bwd_rows_mnmajor(r, status, num_sms, st));
     }
-    if (R > 0) {
+    if (saved) {
+        SwigluBwdSaved p = *a.saved_routed;
+        p.u = b.dh_pad;
+        p.prow = b.prow;
+        p.prow_rows = Rp;
+        p.perm = b.perm;
+        p.w = a.w;
+        p.dadg = b.dadg;
+        p.h = b.h_pad;
+        p.dw = b.dw;
+        p.status = status;
+        TC_TRY(launch_swiglu_bwd_saved(p, st));
+        TC_TRY(dw2());
+    } else if (R > 0) {
         swiglu_bwd_dw_pad_kernel<<<(R + 7) / 8, 256, 0, st>>>(b.a_pad, b.g_pad, b.dh_pad, b.prow, b.perm, a.w, R, I,
                                                               b.dadg, b.dw);
         note_launches(1);
@@ -1019,20 +1095,33 @@ cudaError_t experts_backward_tc(const BackwardArgs& a, const BwdBufs& b, int* st
                                                                   reinterpret_cast<__nv_bfloat16*>(b.dys16));
         note_launches(1);
         const size_t eb = 2;
+        // dWs2_s = dy^T hs_s
+        const auto dws2 = [&](int s) {
+            return launch_bwd_wgrad(wgrad_args(b.dys16, d, 0, b.hs16, SI, (long long)s * Is, T, d, Is,
+                                               a.dws2 + (size_t)s * d * Is, false),
+                                    status, num_sms, st);
+        };
         for (int s = 0; s < S; ++s) {
             const char* w2s = static_cast<const char*>(a.ws2) + eb * (size_t)s * d * Is;
-            // dWs2_s = dy^T hs_s
-            TC_TRY(launch_bwd_wgrad(wgrad_args(b.dys16, d, 0, b.hs16, SI, (long long)s * Is, T, d, Is,
-                                               a.dws2 + (size_t)s * d * Is, false),
-                                    status, num_sms, st));
+            if (!saved) TC_TRY(dws2(s));
             // dhs_s = dy Ws2_s
             BwdRowsArgs r = rows_args(w2s, d, 0, b.dys16, T, d, Is, b.dhs32 + (size_t)s * Is, false);
             r.ldo = SI;
             TC_TRY(launch_bwd_rows_mnmajor(r, status, num_sms, st));
         }
-        swiglu_bwd_pad_kernel<<<ew_grid((long long)T * SI / 4), 256, 0, st>>>(b.as32, b.gs32, b.dhs32, nullptr, T,
-                                                                              SI, b.dadgs);
-        note_launches(1);
+        if (saved) {
+            SwigluBwdSaved p = *a.saved_shared;
+            p.u = b.dhs32;
+            p.dadg = b.dadgs;
+            p.h = b.hs16;
+            p.status = status;
+            TC_TRY(launch_swiglu_bwd_saved(p, st));
+            for (int s = 0; s < S; ++s) TC_TRY(dws2(s));
+        } else {
+            swiglu_bwd_pad_kernel<<<ew_grid((long long)T * SI / 4), 256, 0, st>>>(b.as32, b.gs32, b.dhs32, nullptr, T,
+                                                                                  SI, b.dadgs);
+            note_launches(1);
+        }
         TC_TRY(launch_bwd_wgrad(wgrad_args(b.dadgs, 2 * SI, 0, a.x, d, 0, T, SI, d, a.dws1, false), status, num_sms,
                                 st));
         TC_TRY(launch_bwd_wgrad(wgrad_args(b.dadgs, 2 * SI, SI, a.x, d, 0, T, SI, d, a.dws3, false), status, num_sms,
@@ -1056,7 +1145,9 @@ cudaError_t launch_layer_backward(const BackwardArgs& a, int* status, int num_sm
     const int nb = a.alpha > 0.0f ? T / a.seq_len : 0;
     const bool tc = backward_on_tensor_cores(bf, d, I, S, Is);
     BwdBufs bb;
-    carve(&bb, static_cast<char*>(a.workspace), T, d, E, k, I, S, Is, a.alpha > 0.0f ? a.seq_len : 0, tc);
+    const bool logits = a.logits != nullptr;
+    carve(&bb, static_cast<char*>(a.workspace), T, d, E, k, I, S, Is, a.alpha > 0.0f ? a.seq_len : 0, tc, logits,
+          a.saved_routed != nullptr);
     int32_t* offsets = bb.offsets;
     int32_t* perm = bb.perm;
     int32_t* inv = bb.inv;
@@ -1085,6 +1176,11 @@ cudaError_t launch_layer_backward(const BackwardArgs& a, int* status, int num_sm
         if ((err = (x)) != cudaSuccess) return err; \
     } while (0)
 
+    if (logits && R > 0) {  // a token with fewer than k experts leaves entries unset: they read as none
+        BWD_TRY(cudaMemsetAsync(perm, 0xff, (size_t)R * 4, st));
+        BWD_TRY(cudaMemsetAsync(inv, 0xff, (size_t)R * 4, st));
+        if (tc) BWD_TRY(cudaMemsetAsync(bb.prow, 0xff, (size_t)R * 4, st));
+    }
     // routing layout of the forward: offsets, perm_tok, inv_row (no row copy)
     BWD_TRY(launch_permute(nullptr, a.idx, a.counts, T, d, E, k, bf ? 2 : 4, nullptr, offsets, perm, inv, pscratch,
                            status, st));
@@ -1166,12 +1262,25 @@ cudaError_t launch_layer_backward(const BackwardArgs& a, int* status, int num_sm
             seq_counts_kernel<<<ew_grid((long long)R), 256, 0, st>>>(a.idx, T, k, E, a.seq_len, cnt, status);
             note_launches(1);
         }
-        router_bwd_kernel<<<(T + 7) / 8, 256, 0, st>>>(a.s, a.idx, dw, nb > 0 ? cnt : nullptr, a.alpha, a.seq_len,
-                                                        nb, T, E, k, dz, tot, status);
-        note_launches(1);
+        const float* scores = a.s;
+        if (logits) {
+            const float* dscores = a.dscores;
+            if (nb > 0) {
+                scores_kernel<<<(T + 7) / 8, 256, 0, st>>>(a.logits, a.dscores, cnt, a.alpha, a.seq_len, nb, T, E, k,
+                                                           a.opts.softmax, bb.scores, tot, bb.dscores);
+                note_launches(1);
+                scores = bb.scores;
+                dscores = bb.dscores;
+            }
+            BWD_TRY(launch_route_logits_bwd(a.logits, a.idx, dw, dscores, T, E, k, a.opts, dz, status, st));
+        } else {
+            router_bwd_kernel<<<(T + 7) / 8, 256, 0, st>>>(a.s, a.idx, dw, nb > 0 ? cnt : nullptr, a.alpha,
+                                                            a.seq_len, nb, T, E, k, dz, tot, status);
+            note_launches(1);
+        }
         if (nb > 0 && a.loss) {
             const size_t gsm = (size_t)(256 / E) * E * sizeof(float);  // E <= 256
-            balance_chunk_kernel<<<dim3((unsigned)C, (unsigned)nb), 256, gsm, st>>>(a.s, tot, a.seq_len, E, C, chunk);
+            balance_chunk_kernel<<<dim3((unsigned)C, (unsigned)nb), 256, gsm, st>>>(scores, tot, a.seq_len, E, C, chunk);
             balance_part_kernel<<<nb, 256, gsm, st>>>(chunk, cnt, a.alpha, a.seq_len, E, k, C, part);
             balance_sum_kernel<<<1, 32, 0, st>>>(part, nb, a.loss);
             note_launches(3);

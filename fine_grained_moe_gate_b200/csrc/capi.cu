@@ -898,8 +898,166 @@ moe_status moe_swiglu_backward_saved(const moe_saved_acts* saved, moe_shape sh, 
     p.h = static_cast<uint16_t*>(h);
     p.dw = dw;
     p.status = status;
-    return moe::launch_swiglu_bwd_saved(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+    return moe::launch_swiglu_bwd_saved(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
                                                                                                   : MOE_ERR_CUDA;
+}
+
+// ---- the layer with routing from logits ----------------------------------------
+
+moe_status moe_layer_forward_logits(const void* x, const void* w_gate, const float* bias, const void* w1,
+                                    const void* w3, const void* w2, const void* ws1, const void* ws3, const void* ws2,
+                                    moe_shape sh, moe_route_opts opts, void* y, float* logits, int32_t* topk_idx,
+                                    float* topk_w, int32_t* counts, const moe_saved_acts* saved, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+    moe_status v = validate_dense_weights(sh);
+    if (v == MOE_OK) v = validate_opts(opts, sh);
+    if (v != MOE_OK) return v;
+    MOE_REQUIRE(!saved || sh.dtype == MOE_BF16, MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(w_gate && w1 && w3 && w2 && counts, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.S == 0 || (ws1 && ws3 && ws2), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || (x && y && logits && topk_idx && topk_w), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || !saved || (saved_ok(*saved, false) && (sh.S == 0 || saved_ok(*saved, true))),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(x) && aligned16(w_gate) && aligned16(bias) && aligned16(w1) && aligned16(w3) &&
+                    aligned16(w2) && aligned16(ws1) && aligned16(ws3) && aligned16(ws2) && aligned16(y) &&
+                    aligned16(logits) && aligned16(topk_idx) && aligned16(topk_w) && aligned16(counts) &&
+                    (!saved || saved_aligned(*saved)),
+                MOE_ERR_ALIGNMENT);
+    const size_t need = moe_workspace_size(sh);
+    MOE_REQUIRE(workspace && ws_bytes >= need, MOE_ERR_WORKSPACE);
+    MOE_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+    // the workspace of moe_layer_forward
+    const size_t rows = (size_t)sh.T * sh.k, eb = esize(sh);
+    char* p = static_cast<char*>(workspace);
+    const auto take = [&p](size_t bytes) {
+        char* q = p;
+        p += align256(bytes);
+        return q;
+    };
+    int32_t* offsets = reinterpret_cast<int32_t*>(take((sh.E + 1) * sizeof(int32_t)));
+    int32_t* perm = reinterpret_cast<int32_t*>(take(rows * sizeof(int32_t)));
+    int32_t* inv = reinterpret_cast<int32_t*>(take(rows * sizeof(int32_t)));
+    void* pws = take(permute_ws(sh));
+    void* x_perm = take(rows * sh.d * eb);  // then y_perm
+    void* h = take(rows * sh.I * eb);
+    void* hs = take((size_t)sh.T * sh.S * (size_t)sh.Is * eb);
+    void* shared_out = sh.S > 0 ? take((size_t)sh.T * sh.d * eb) : nullptr;
+
+    if ((v = do_gate_logits(x, w_gate, sh, logits, status, sms, st)) != MOE_OK) return v;
+    MOE_CUDA(moe::launch_route_logits(logits, bias, sh.T, sh.E, sh.k, route_opts(opts), topk_idx, topk_w, counts,
+                                      status, sms, st));
+    if (sh.T == 0) return MOE_OK;
+    // a token with fewer than k experts leaves its entries of inv unset: they read as none
+    MOE_CUDA(cudaMemsetAsync(inv, 0xff, rows * sizeof(int32_t), st));
+    if ((v = do_permute(x, topk_idx, counts, sh, x_perm, offsets, perm, inv, pws, status, st)) != MOE_OK) return v;
+    const void* xs = sh.S > 0 ? x : nullptr;
+    v = saved ? do_ffn_up_save(x_perm, offsets, w1, w3, xs, ws1, ws3, sh, h, hs, *saved, status, sms, st)
+              : do_ffn_up(x_perm, offsets, w1, w3, xs, ws1, ws3, sh, h, hs, status, sms, st);
+    if (v != MOE_OK) return v;
+    if ((v = do_ffn_down(h, offsets, w2, sh.S > 0 ? hs : nullptr, ws2, sh, x_perm, shared_out, status, sms, st)) !=
+        MOE_OK)
+        return v;
+    return moe::launch_combine(x_perm, topk_w, inv, shared_out, sh.T, sh.d, sh.k, sh.dtype != MOE_F32, y, status,
+                               st) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+size_t moe_backward_logits_workspace_size(moe_shape sh, int32_t seq_len, int32_t saved) {
+    if (validate_dense_weights(sh) != MOE_OK) return 0;
+    if (saved && !moe::backward_on_tensor_cores(sh.dtype == MOE_BF16, sh.d, sh.I, sh.S, sh.Is)) return 0;
+    return moe::backward_scratch_bytes(sh.T, sh.d, sh.E, sh.k, sh.I, sh.S, sh.Is, seq_len > 0 ? seq_len : 0,
+                                       sh.dtype == MOE_BF16, true, saved != 0);
+}
+
+moe_status moe_layer_backward_logits(const void* x, const void* w_gate, const void* w1, const void* w3,
+                                     const void* w2, const void* ws1, const void* ws3, const void* ws2, moe_shape sh,
+                                     moe_route_opts opts, const moe_saved_acts* saved, const float* logits,
+                                     const int32_t* topk_idx, const float* topk_w, const int32_t* counts,
+                                     const float* dscores, const float* dy, float alpha, int32_t seq_len, float* dx,
+                                     float* dw_gate, float* dw1, float* dw3, float* dw2, float* dws1, float* dws3,
+                                     float* dws2, float* balance_loss, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+    moe_status v = validate_dense_weights(sh);
+    if (v == MOE_OK) v = validate_opts(opts, sh);
+    if (v != MOE_OK) return v;
+    const bool bf16 = sh.dtype == MOE_BF16;
+    MOE_REQUIRE(!saved || moe::backward_on_tensor_cores(bf16, sh.d, sh.I, sh.S, sh.Is), MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(w_gate && w1 && w3 && w2 && counts && dw_gate && dw1 && dw3 && dw2, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || (x && logits && topk_idx && topk_w && dy && dx), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.S == 0 || (ws1 && ws3 && ws2 && dws1 && dws3 && dws2), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(sh.T == 0 || !saved || (saved_ok(*saved, false) && (sh.S == 0 || saved_ok(*saved, true))),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(alpha == alpha && alpha >= 0.0f && alpha < 3.0e38f, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(alpha == 0.0f || (seq_len > 0 && sh.T % seq_len == 0), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(alpha == 0.0f || sh.T / seq_len <= 65535, MOE_ERR_UNSUPPORTED);  // sequences per launch
+    MOE_REQUIRE(aligned16(x) && aligned16(w_gate) && aligned16(w1) && aligned16(w3) && aligned16(w2) &&
+                    aligned16(ws1) && aligned16(ws3) && aligned16(ws2) && aligned16(logits) && aligned16(topk_idx) &&
+                    aligned16(topk_w) && aligned16(counts) && aligned16(dscores) && aligned16(dy) && aligned16(dx) &&
+                    aligned16(dw_gate) && aligned16(dw1) && aligned16(dw3) && aligned16(dw2) && aligned16(dws1) &&
+                    aligned16(dws3) && aligned16(dws2) && (!saved || saved_aligned(*saved)),
+                MOE_ERR_ALIGNMENT);
+    const int32_t L = alpha > 0.0f ? seq_len : 0;
+    const size_t need = moe_backward_logits_workspace_size(sh, L, saved != nullptr);
+    MOE_REQUIRE(workspace && ws_bytes >= need, MOE_ERR_WORKSPACE);
+    MOE_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, MOE_ERR_ALIGNMENT);
+    int dev, sms;
+    int* status;
+    v = device_setup(&dev, &status, &sms);
+    if (v != MOE_OK) return v;
+    moe::SwigluBwdSaved routed{}, shared{};
+    if (saved) {
+        routed = saved_bwd_args(*saved, sh, false);
+        shared = saved_bwd_args(*saved, sh, true);
+    }
+    moe::BackwardArgs a{};
+    a.x = x;
+    a.w_gate = w_gate;
+    a.w1 = w1;
+    a.w3 = w3;
+    a.w2 = w2;
+    a.ws1 = ws1;
+    a.ws3 = ws3;
+    a.ws2 = ws2;
+    a.T = sh.T;
+    a.d = sh.d;
+    a.E = sh.E;
+    a.k = sh.k;
+    a.I = sh.I;
+    a.S = sh.S;
+    a.Is = sh.Is;
+    a.bf16 = bf16;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    a.counts = counts;
+    a.dy = dy;
+    a.alpha = alpha;
+    a.seq_len = L;
+    a.dx = dx;
+    a.dw_gate = dw_gate;
+    a.dw1 = dw1;
+    a.dw3 = dw3;
+    a.dw2 = dw2;
+    a.dws1 = dws1;
+    a.dws3 = dws3;
+    a.dws2 = dws2;
+    a.loss = balance_loss;
+    a.workspace = workspace;
+    a.num_sms = sms;
+    a.logits = logits ? logits : reinterpret_cast<const float*>(workspace);  // T == 0: read by nobody
+    a.dscores = dscores;
+    a.opts = route_opts(opts);
+    a.saved_routed = saved ? &routed : nullptr;
+    a.saved_shared = saved ? &shared : nullptr;
+    return moe::launch_layer_backward(a, status, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 size_t moe_fp8_scale_bytes(int64_t rows, int32_t K, int32_t layout) {

@@ -96,6 +96,7 @@ struct SwigluBwdSaved {
     const uint8_t *a, *a_scale, *g, *g_scale;
     const float* u;
     const int32_t* prow;
+    long long prow_rows;  // rows that u, dadg and h have when prow is given
     const int32_t* perm;
     const float* w;
     uint16_t* dadg;
@@ -105,7 +106,7 @@ struct SwigluBwdSaved {
     int n;
     int* status;
 };
-cudaError_t launch_swiglu_bwd_saved(const SwigluBwdSaved& p, int num_sms, cudaStream_t st);
+cudaError_t launch_swiglu_bwd_saved(const SwigluBwdSaved& p, cudaStream_t st);
 
 // permute.cu
 size_t permute_scratch_bytes(int T, int E);
@@ -129,8 +130,18 @@ struct BackwardArgs {
     float *dx, *dw_gate, *dw1, *dw3, *dw2, *dws1, *dws3, *dws2, *loss;
     void* workspace;
     int num_sms;
+    // Routing from logits (logits non-null; s is then unused): its form, and
+    // an upstream gradient of the scores [T][E] (may be null).
+    const float* logits;
+    const float* dscores;
+    RouteOpts opts;
+    // The forward's pre-activations in 8 bits (tensor-core path only), or null:
+    // recompute them.  Codes and scales only; shared unused when S == 0.
+    const SwigluBwdSaved* saved_routed;
+    const SwigluBwdSaved* saved_shared;
 };
-size_t backward_scratch_bytes(int T, int d, int E, int k, int I, int S, int Is, int seq_len, bool bf16);
+size_t backward_scratch_bytes(int T, int d, int E, int k, int I, int S, int Is, int seq_len, bool bf16,
+                              bool logits = false, bool saved = false);
 bool backward_on_tensor_cores(bool bf16, int d, int I, int S, int Is);
 cudaError_t launch_layer_backward(const BackwardArgs& a, int* status, int num_sms, cudaStream_t st);
 

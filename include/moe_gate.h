@@ -480,8 +480,8 @@ MOE_API moe_status moe_gate_logits(const void* x, const void* w_gate, moe_shape 
  * The order is that of the 64-bit values: v closer to each other than the
  * error of their 32-bit form is evaluated again in 64 bits.
  * An expert with logit -inf, or with v -inf (bias -inf), is masked: it has no
- * score, is never chosen and counts in no group value.  A NaN logit is masked
- * too and reported (MOE_ERR_DEVICE_CHECK via moe_get_last_error).  A token
+ * score, is never chosen and counts in no group value.  A NaN logit or
+ * bias is masked too and reported (MOE_ERR_DEVICE_CHECK via moe_get_last_error).  A token
  * with fewer than k experts to choose from gets index -1 and weight 0 in the
  * slots left, and is reported likewise.  logit +inf: the limit of the formula.
  * logits [T][E] fp32; of sh only T, E and k matter here (the rest has to be
@@ -541,6 +541,39 @@ MOE_API moe_status moe_ffn_up_save(const void* x_perm, const int32_t* offsets, c
 MOE_API moe_status moe_swiglu_backward_saved(const moe_saved_acts* saved, moe_shape sh, int32_t set, const float* u,
                                              const int32_t* perm_tok, const float* topk_w, void* dadg, void* h,
                                              float* dw, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_layer_forward_logits / moe_layer_backward_logits -- the layer and its
+ * gradients with routing from logits, in any of its forms, and with or without
+ * saved activations.
+ *   forward: moe_gate_logits (into logits [T][E], kept for the backward),
+ *     moe_route_logits, moe_permute, moe_ffn_up_save (saved != NULL; bf16
+ *     layers) or moe_ffn_up, moe_ffn_down, moe_combine.  bias may be NULL.
+ *     A token with fewer than k experts to choose from (reported) gets the sum
+ *     over those it has.  workspace >= moe_workspace_size(sh) bytes.
+ *   backward: as moe_layer_backward, for <dy, y> + <dscores, s> +
+ *     balance_loss (s the scores of the gate's form; dscores may be NULL), the
+ *     router's part by moe_route_logits_backward.  saved: the forward's, read in
+ *     place of running its gate/up product again (bf16 layers whose d, I and Is
+ *     are multiples of 128, MOE_ERR_UNSUPPORTED otherwise); NULL: recompute.
+ *     workspace >= moe_backward_logits_workspace_size(sh, seq_len, saved != NULL)
+ *     bytes (seq_len 0 when alpha == 0; 0 if the layer cannot be served).
+ * -------------------------------------------------------------------------*/
+MOE_API moe_status moe_layer_forward_logits(const void* x, const void* w_gate, const float* bias, const void* w1,
+                                            const void* w3, const void* w2, const void* ws1, const void* ws3,
+                                            const void* ws2, moe_shape sh, moe_route_opts opts, void* y, float* logits,
+                                            int32_t* topk_idx, float* topk_w, int32_t* counts,
+                                            const moe_saved_acts* saved, void* workspace, size_t ws_bytes,
+                                            void* stream);
+MOE_API size_t moe_backward_logits_workspace_size(moe_shape sh, int32_t seq_len, int32_t saved);
+MOE_API moe_status moe_layer_backward_logits(const void* x, const void* w_gate, const void* w1, const void* w3,
+                                             const void* w2, const void* ws1, const void* ws3, const void* ws2,
+                                             moe_shape sh, moe_route_opts opts, const moe_saved_acts* saved,
+                                             const float* logits, const int32_t* topk_idx, const float* topk_w,
+                                             const int32_t* counts, const float* dscores, const float* dy, float alpha,
+                                             int32_t seq_len, float* dx, float* dw_gate, float* dw1, float* dw3,
+                                             float* dw2, float* dws1, float* dws3, float* dws2, float* balance_loss,
+                                             void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Expert parallelism (no counterpart in the pages' code; their "custom

@@ -153,3 +153,40 @@ def test_binding_helpers():
     assert buf["sg"].shape == (128, 256) and buf["sg_scale"].numel() == 2 * 128 * 4
     s = moe.saved_acts(buf)
     assert s.sa == buf["sa"].data_ptr()
+
+
+def test_layer_refusals(L):
+    sh, need = shape(), moe.moe_workspace_size(shape())
+
+    def fwd(sh=sh, o=opts(), saved=_saved(), bias=FAKE, logits=FAKE, ws=FAKE, n=need, ws1=FAKE):
+        return L.moe_layer_forward_logits(c(FAKE), c(FAKE), c(bias), c(FAKE), c(FAKE), c(FAKE), c(ws1), c(FAKE), c(FAKE),
+                                          sh, o, c(FAKE), c(logits), c(FAKE), c(FAKE), c(FAKE),
+                                          ctypes.byref(saved) if saved is not None else None, c(ws), n, None)
+
+    assert fwd(o=opts(groups=3)) == INVALID
+    assert fwd(logits=None) == INVALID and fwd(ws1=None) == INVALID
+    assert fwd(logits=FAKE + 4) == ALIGN and fwd(bias=FAKE + 4) == ALIGN
+    assert fwd(n=need - 256) == WORKSPACE and fwd(ws=None) == WORKSPACE and fwd(ws=FAKE + 16) == ALIGN
+    assert fwd(saved=_saved(sg=None)) == INVALID and fwd(saved=_saved(g_scale=FAKE + 4)) == ALIGN
+    assert fwd(sh=shape(dtype=moe.MOE_F32)) == UNSUPPORTED  # saved activations are a bf16 layer's
+    assert fwd(sh=shape(dtype=moe.MOE_FP8_E4M3), saved=None) == UNSUPPORTED
+
+    def bwd(sh=sh, o=opts(), saved=_saved(), logits=FAKE, ds=None, alpha=0.0, seq=0, n=None, dx=FAKE):
+        if n is None:
+            n = moe.moe_backward_logits_workspace_size(sh, seq, saved is not None)
+        return L.moe_layer_backward_logits(*[c(FAKE)] * 8, sh, o, ctypes.byref(saved) if saved is not None else None,
+                                           c(logits), c(FAKE), c(FAKE), c(FAKE), c(ds), c(FAKE), alpha, seq, c(dx),
+                                           *[c(FAKE)] * 7, None, c(FAKE), n, None)
+
+    assert bwd(o=opts(scale=float("inf"))) == INVALID
+    assert bwd(logits=None) == INVALID and bwd(dx=None) == INVALID and bwd(saved=_saved(a=None)) == INVALID
+    assert bwd(logits=FAKE + 4) == ALIGN and bwd(ds=FAKE + 4) == ALIGN
+    assert bwd(alpha=-1.0) == INVALID and bwd(alpha=0.1, seq=0) == INVALID and bwd(alpha=0.1, seq=100) == INVALID
+    assert bwd(n=moe.moe_backward_logits_workspace_size(sh, 0, True) - 256) == WORKSPACE
+    assert bwd(alpha=0.1, seq=64, n=moe.moe_backward_logits_workspace_size(sh, 0, True)) == WORKSPACE
+    assert bwd(sh=shape(d=192)) == UNSUPPORTED  # saved activations need the tensor-core widths
+    assert bwd(sh=shape(dtype=moe.MOE_F32)) == UNSUPPORTED
+    assert moe.moe_backward_logits_workspace_size(shape(d=192), 0, True) == 0
+    assert moe.moe_backward_logits_workspace_size(shape(d=192), 0, False) > 0
+    full, less = (moe.moe_backward_logits_workspace_size(sh, 0, f) for f in (False, True))
+    assert full - less >= 2 * 4 * (512 * 128 + 128 * 128)  # no fp32 a and g
