@@ -198,10 +198,13 @@ def _p(t):
     return t if isinstance(t, int) else t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if device is None:
+            device = torch.cuda.current_device()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without a Stream object (3 us)
+        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -212,6 +215,48 @@ def _check(status: int, where: str):
 
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
+
+
+_dtypes: dict = {}
+
+
+def _call(name, stream, *args):
+    """Call entry point ``name`` on the given arguments and the stream.  A tuple
+    (argument name, tensor, dtype, elements) is checked before it is passed as
+    a pointer: the dtype, a contiguous tensor of at least so many elements, on
+    the device of the others.  None and raw pointers go through as they are.
+    The call runs with the tensors' device current, on its current stream
+    unless one is given."""
+    import torch
+    if not _dtypes:
+        _dtypes.update((n, getattr(torch, n)) for n in ("float32", "bfloat16", "int32", "uint8"))
+    dev, out = -1, []
+    for a in args:
+        if type(a) is tuple:
+            what, a, dtype, n = a
+            if a is not None and type(a) is not int:
+                if a.dtype is not _dtypes[dtype]:
+                    raise MoEError(1, f"{name}: {what} must be {dtype}, got {a.dtype}")
+                if a.numel() < n or not a.is_contiguous():
+                    raise MoEError(1, f"{name}: {what} must be contiguous with at least {n} elements, got "
+                                      f"{tuple(a.shape)}, strides {a.stride()}")
+                d = a.get_device()
+                if d < 0 or 0 <= dev != d:
+                    raise MoEError(1, f"{name}: {what} must be on one CUDA device with the other tensors, got {a.device}")
+                dev = d
+                a = a.data_ptr()
+        out.append(a)
+    fn = getattr(lib(), name)
+    if dev < 0 or dev == torch.cuda.current_device():
+        _check(fn(*out, _stream(stream, dev if dev >= 0 else None)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*out, _stream(stream, dev)), name)
+
+
+def _dt(shape) -> str:
+    """dtype of x, the dense weights and the activations of a layer."""
+    return "float32" if shape.dtype == MOE_F32 else "bfloat16"
 
 
 # ---- entry points (same names and argument order as moe_gate.h) -----------
@@ -437,17 +482,22 @@ def quantize_experts_fp8(p: dict, stream=None) -> dict:
 # ---- routing from logits -----------------------------------------------------
 
 def moe_gate_logits(x, w_gate, shape, logits, stream=None):
-    _check(lib().moe_gate_logits(_p(x), _p(w_gate), shape, _p(logits), _stream(stream)), "moe_gate_logits")
+    T, d, E, dt = shape.T, shape.d, shape.E, _dt(shape)
+    _call("moe_gate_logits", stream, ("x", x, dt, T * d), ("w_gate", w_gate, dt, E * d), shape,
+          ("logits", logits, "float32", T * E))
 
 
 def moe_route_logits(logits, bias, shape, opts, topk_idx, topk_w, counts, stream=None):
-    _check(lib().moe_route_logits(_p(logits), _p(bias), shape, opts, _p(topk_idx), _p(topk_w), _p(counts),
-                                  _stream(stream)), "moe_route_logits")
+    T, E, k = shape.T, shape.E, shape.k
+    _call("moe_route_logits", stream, ("logits", logits, "float32", T * E), ("bias", bias, "float32", E), shape, opts,
+          ("topk_idx", topk_idx, "int32", T * k), ("topk_w", topk_w, "float32", T * k), ("counts", counts, "int32", E))
 
 
 def moe_route_logits_backward(logits, topk_idx, dw, dscores, shape, opts, dlogits, stream=None):
-    _check(lib().moe_route_logits_backward(_p(logits), _p(topk_idx), _p(dw), _p(dscores), shape, opts, _p(dlogits),
-                                           _stream(stream)), "moe_route_logits_backward")
+    T, E, k = shape.T, shape.E, shape.k
+    _call("moe_route_logits_backward", stream, ("logits", logits, "float32", T * E),
+          ("topk_idx", topk_idx, "int32", T * k), ("dw", dw, "float32", T * k), ("dscores", dscores, "float32", T * E),
+          shape, opts, ("dlogits", dlogits, "float32", T * E))
 
 
 # ---- activations saved in 8 bits -----------------------------------------------
@@ -468,23 +518,45 @@ def saved_act_buffers(shape, device) -> dict:
 
 
 def moe_ffn_up_save(x_perm, offsets, w1, w3, x, ws1, ws3, shape, h, hs, saved, stream=None):
-    _check(lib().moe_ffn_up_save(_p(x_perm), _p(offsets), _p(w1), _p(w3), _p(x), _p(ws1), _p(ws3), shape, _p(h),
-                                 _p(hs), ctypes.byref(saved), _stream(stream)), "moe_ffn_up_save")
+    T, d, E, dt, SI = shape.T, shape.d, shape.E, _dt(shape), shape.S * shape.Is
+    R, I = T * shape.k, shape.I
+    _call("moe_ffn_up_save", stream, ("x_perm", x_perm, dt, R * d), ("offsets", offsets, "int32", E + 1),
+          ("w1", w1, dt, E * I * d), ("w3", w3, dt, E * I * d), ("x", x, dt, T * d), ("ws1", ws1, dt, SI * d),
+          ("ws3", ws3, dt, SI * d), shape, ("h", h, dt, R * I), ("hs", hs, dt, T * SI), ctypes.byref(saved))
 
 
 def moe_swiglu_backward_saved(saved, shape, expert_set, u, perm_tok, topk_w, dadg, h, dw, stream=None):
-    _check(lib().moe_swiglu_backward_saved(ctypes.byref(saved), shape, expert_set, _p(u), _p(perm_tok), _p(topk_w),
-                                           _p(dadg), _p(h), _p(dw), _stream(stream)), "moe_swiglu_backward_saved")
+    R = shape.T * shape.k
+    n = R * shape.I if expert_set == MOE_ROUTED else shape.T * shape.S * shape.Is
+    _call("moe_swiglu_backward_saved", stream, ctypes.byref(saved), shape, expert_set, ("u", u, "float32", n),
+          ("perm_tok", perm_tok, "int32", R), ("topk_w", topk_w, "float32", R), ("dadg", dadg, "bfloat16", 2 * n),
+          ("h", h, "bfloat16", n), ("dw", dw, "float32", R))
 
 
 # ---- the layer with routing from logits ------------------------------------------
 
+def _layer_args(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape):
+    """The checked weights of a layer, by name."""
+    dt, d, SI = _dt(shape), shape.d, shape.S * shape.Is
+    EId = shape.E * shape.I * d
+    return dict(x=("x", x, dt, shape.T * d), w_gate=("w_gate", w_gate, dt, shape.E * d), w1=("w1", w1, dt, EId),
+                w3=("w3", w3, dt, EId), w2=("w2", w2, dt, EId), ws1=("ws1", ws1, dt, SI * d),
+                ws3=("ws3", ws3, dt, SI * d), ws2=("ws2", ws2, dt, SI * d))
+
+
+def _saved_ref(saved):
+    return None if saved is None else ctypes.byref(saved)
+
+
 def moe_layer_forward_logits(x, w_gate, bias, w1, w3, w2, ws1, ws3, ws2, shape, opts, y, logits, topk_idx, topk_w,
                              counts, saved, workspace, stream=None):
-    _check(lib().moe_layer_forward_logits(_p(x), _p(w_gate), _p(bias), _p(w1), _p(w3), _p(w2), _p(ws1), _p(ws3),
-                                          _p(ws2), shape, opts, _p(y), _p(logits), _p(topk_idx), _p(topk_w),
-                                          _p(counts), None if saved is None else ctypes.byref(saved), _p(workspace),
-                                          _nbytes(workspace), _stream(stream)), "moe_layer_forward_logits")
+    T, E, k = shape.T, shape.E, shape.k
+    a = _layer_args(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape)
+    _call("moe_layer_forward_logits", stream, a["x"], a["w_gate"], ("bias", bias, "float32", E), a["w1"], a["w3"],
+          a["w2"], a["ws1"], a["ws3"], a["ws2"], shape, opts, ("y", y, _dt(shape), T * shape.d),
+          ("logits", logits, "float32", T * E), ("topk_idx", topk_idx, "int32", T * k),
+          ("topk_w", topk_w, "float32", T * k), ("counts", counts, "int32", E), _saved_ref(saved),
+          ("workspace", workspace, "uint8", 0), _nbytes(workspace))
 
 
 def moe_backward_logits_workspace_size(shape, seq_len: int = 0, saved: bool = False) -> int:
@@ -494,12 +566,17 @@ def moe_backward_logits_workspace_size(shape, seq_len: int = 0, saved: bool = Fa
 def moe_layer_backward_logits(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape, opts, saved, logits, topk_idx, topk_w,
                               counts, dscores, dy, alpha, seq_len, dx, dw_gate, dw1, dw3, dw2, dws1, dws3, dws2,
                               balance_loss, workspace, stream=None):
-    _check(lib().moe_layer_backward_logits(_p(x), _p(w_gate), _p(w1), _p(w3), _p(w2), _p(ws1), _p(ws3), _p(ws2),
-                                           shape, opts, None if saved is None else ctypes.byref(saved), _p(logits),
-                                           _p(topk_idx), _p(topk_w), _p(counts), _p(dscores), _p(dy), float(alpha),
-                                           int(seq_len), _p(dx), _p(dw_gate), _p(dw1), _p(dw3), _p(dw2), _p(dws1),
-                                           _p(dws3), _p(dws2), _p(balance_loss), _p(workspace), _nbytes(workspace),
-                                           _stream(stream)), "moe_layer_backward_logits")
+    T, d, E, k, SI = shape.T, shape.d, shape.E, shape.k, shape.S * shape.Is
+    EId = E * shape.I * d
+    f = lambda name, t, n: (name, t, "float32", n)
+    a = _layer_args(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape)
+    _call("moe_layer_backward_logits", stream, a["x"], a["w_gate"], a["w1"], a["w3"], a["w2"], a["ws1"], a["ws3"],
+          a["ws2"], shape, opts, _saved_ref(saved), f("logits", logits, T * E), ("topk_idx", topk_idx, "int32", T * k),
+          f("topk_w", topk_w, T * k), ("counts", counts, "int32", E), f("dscores", dscores, T * E), f("dy", dy, T * d),
+          float(alpha), int(seq_len), f("dx", dx, T * d), f("dw_gate", dw_gate, E * d), f("dw1", dw1, EId),
+          f("dw3", dw3, EId), f("dw2", dw2, EId), f("dws1", dws1, SI * d), f("dws3", dws3, SI * d),
+          f("dws2", dws2, SI * d), f("balance_loss", balance_loss, 1), ("workspace", workspace, "uint8", 0),
+          _nbytes(workspace))
 
 
 # ---- expert parallelism --------------------------------------------------------

@@ -422,3 +422,30 @@ def test_other_stream_and_graph_replay():
         tol = _grad_bound(z.cpu().numpy(), idx.cpu().numpy(), dw.cpu().numpy().astype(np.float64), None, o)
         assert (np.abs(dz.cpu().numpy() - ref) <= tol).all()
     check_status()
+
+
+def test_streams_and_strided_inputs():
+    """A stream of the caller's; two batches on two streams at once; a strided tensor is refused."""
+    o = OPTS["groups2"]
+    co = c_opts(o)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for i, st in enumerate(streams):
+        T, E, k = 3000 + i, 256, 8
+        z, bias = make(T, E, 30 + i)
+        runs.append((z, bias, torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV),
+                     torch.empty(E, dtype=torch.int32, device=DEV)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (z, bias, idx, w, counts) in zip(streams, runs):
+            moe.moe_route_logits(z, bias, shape(z.shape[0], 256, 8), co, idx, w, counts, stream=st)
+    with torch.cuda.stream(streams[0]):  # the current stream, when none is given
+        moe.moe_route_logits(runs[0][0], runs[0][1], shape(3000, 256, 8), co, *runs[0][2:])
+    torch.cuda.synchronize()
+    for z, bias, idx, w, counts in runs:
+        check_route(z, bias, 8, o, (idx.cpu().numpy(), w.cpu().numpy(), counts.cpu().numpy()))
+    check_status()
+    z, bias, idx, w, counts = runs[0]
+    wide = torch.empty((3000, 512), device=DEV)
+    with pytest.raises(moe.MoEError, match="contiguous"):
+        moe.moe_route_logits(wide[:, :256], bias, shape(3000, 256, 8), co, idx, w, counts)

@@ -190,3 +190,38 @@ def test_layer_refusals(L):
     assert moe.moe_backward_logits_workspace_size(shape(d=192), 0, False) > 0
     full, less = (moe.moe_backward_logits_workspace_size(sh, 0, f) for f in (False, True))
     assert full - less >= 2 * 4 * (512 * 128 + 128 * 128)  # no fp32 a and g
+
+
+def test_binding_refuses_wrong_tensors():
+    """Type, size, strides and device of the tensors, before the library is called (no GPU needed)."""
+    import torch
+    sh = shape()
+    z, idx, w, n = torch.zeros(128, 16), torch.zeros(128, 4, dtype=torch.int32), torch.zeros(128, 4), 16
+    counts = torch.zeros(n, dtype=torch.int32)
+    o = moe.route_opts()
+
+    def refused(match, **kw):
+        a = dict(logits=z, bias=None, idx=idx, w=w, counts=counts)
+        a.update(kw)
+        with pytest.raises(moe.MoEError, match=match) as e:
+            moe.moe_route_logits(a["logits"], a["bias"], sh, o, a["idx"], a["w"], a["counts"])
+        assert e.value.status == INVALID
+
+    refused("logits must be float32", logits=z.double())
+    refused("logits must be contiguous", logits=torch.zeros(16, 128).t())
+    refused("logits must be contiguous with at least 2048", logits=z[:100])
+    refused("logits must be contiguous", logits=torch.zeros(128, 32)[:, :16])
+    refused("one CUDA device", logits=z)
+    bf = torch.zeros(128 * 256, dtype=torch.bfloat16)
+    with pytest.raises(moe.MoEError, match="x must be bfloat16"):
+        moe.moe_gate_logits(bf.float(), bf, sh, z)
+    with pytest.raises(moe.MoEError, match="dlogits|logits"):
+        moe.moe_route_logits_backward(z, idx, w, None, sh, o, z.half())
+    with pytest.raises(moe.MoEError, match="x_perm"):
+        moe.moe_ffn_up_save(bf, counts, bf, bf, None, None, None, sh, bf, None, _saved())
+    with pytest.raises(moe.MoEError, match="u must be float32"):
+        moe.moe_swiglu_backward_saved(_saved(), sh, moe.MOE_ROUTED, bf, idx, w, bf, None, w)
+    with pytest.raises(moe.MoEError, match="x must be"):
+        moe.moe_layer_forward_logits(bf[:5], bf, None, bf, bf, bf, bf, bf, bf, sh, o, bf, z, idx, w, counts, None, bf)
+    with pytest.raises(moe.MoEError, match="x must be"):
+        moe.moe_layer_backward_logits(bf[:5], *[bf] * 7, sh, o, None, z, idx, w, counts, None, z, 0.0, 0, *[z] * 9, bf)
