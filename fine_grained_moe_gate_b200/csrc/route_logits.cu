@@ -84,8 +84,9 @@ struct Cand {
 struct alignas(16) WarpMem {
     double d[kMaxExperts];        // 64-bit values, or all experts' 32-bit values
     Cand cand[kMaxExperts + 2];   // in any order
-    Cand sorted[kMaxK + 2];       // the k + 1 best, descending
+    Cand sorted[kMaxK + 2];       // the k + 1 best, descending (rank_candidates)
     int first[32];                // first expert of each kept group
+    int place[kMaxK + 2];         // lane of the r-th best; expert of the r-th by 64-bit values
 };
 static_assert(sizeof(WarpMem) % 16 == 0, "vector reads in every warp's copy");
 
@@ -96,6 +97,7 @@ struct RouteArgs {
     int per;           // experts of a group
     int per_inv;       // ceil(2^16 / per): e / per = e per_inv >> 16 for e, per <= 256
     int group_lanes;   // lanes that take a group's values, a power of two
+    int direct;        // the kept groups' values are taken where they are, not listed again
     unsigned leaders;  // lane g group_lanes of every group g
     RouteOpts o;
     int32_t* idx;
@@ -167,9 +169,25 @@ __device__ __noinline__ void sort_candidates64(const RouteArgs& a, const float* 
         const int e = wm.cand[c].e;
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += wm.d[j] > v || (wm.d[j] == v && wm.cand[j].e < e);
-        if (rank < a.k) wm.sorted[rank].e = e;
+        if (rank < a.k) wm.place[rank] = e;
     }
     __syncwarp();
+}
+
+// The lanes' experts (lane r < n: e) in the order of their 64-bit values.
+__device__ __noinline__ int reorder64(const RouteArgs& a, const float* row, WarpMem& wm, int e, int n, int lane) {
+    const Softmax64 sm = a.o.softmax ? softmax64(row, a.E, lane) : Softmax64{0.0, 1.0};
+    const double v = lane < n ? value64(a, row, e, sm) : neg_inf64();
+    int rank = 0;
+    for (int r = 0; r < n; ++r) {
+        const double y = __shfl_sync(kFull, v, r);
+        const int f = __shfl_sync(kFull, e, r);
+        rank += y > v || (y == v && f < e);
+    }
+    __syncwarp();
+    if (lane < n) wm.place[rank] = e;
+    __syncwarp();
+    return lane < n ? wm.place[lane] : -1;
 }
 
 // The share of each lane's chosen logit in the sum over the chosen scores of
@@ -438,6 +456,7 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
         if (grouped) {
             float* all = reinterpret_cast<float*>(wm.d);
             const auto put = [&] {  // the row's values where every lane can read them
+                __syncwarp();
                 if (VPT % 4 == 0) {
 #pragma unroll
                     for (int j = 0; j < VPT; j += 4)
@@ -450,16 +469,18 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
                 }
                 __syncwarp();
             };
-            put();
             float x1 = kMasked, x2 = kMasked;
             if (in_lanes) {
                 best2<VPT>(v, x1, x2);
-            } else if (real) {
-                const int last = (my_group + 1) * per;
-                for (int i = my_group * per + sub; i < last; i += LG) {
-                    const float y = all[i];
-                    x2 = fmaxf(x2, fminf(x1, y));
-                    x1 = fmaxf(x1, y);
+            } else {
+                put();
+                if (real) {
+                    const int last = (my_group + 1) * per;
+                    for (int i = my_group * per + sub; i < last; i += LG) {
+                        const float y = all[i];
+                        x2 = fmaxf(x2, fminf(x1, y));
+                        x1 = fmaxf(x1, y);
+                    }
                 }
             }
             for (int o = 1; o < LG; o <<= 1) {
@@ -470,48 +491,53 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
             float gv = a.o.group_top == 2 && x2 > kLow ? x1 + x2 : x1;
             if (!real) gv = kMasked;
             // a group's lanes share the comparison with the others
-            const float err = 3.0f * abs_err + 2.0f * rel_err * fabsf(gv) + 1e-37f;
             int ahead = 0;
-            bool unsure = false;
             for (int i = 0; i < a.o.groups; i += LG) {
                 const float y = __shfl_sync(kFull, gv, ((i + sub) * LG) & 31);
-                const bool other = i + sub < a.o.groups && i + sub != my_group && y > kLow;
-                ahead += other && y > gv;
-                unsure |= other && !(fabsf(y - gv) > fmaf(2.0f * rel_err, fabsf(y), err));
+                ahead += i + sub < a.o.groups && y > gv;
             }
             for (int o = 1; o < LG; o <<= 1) ahead += __shfl_xor_sync(kFull, ahead, o);
-            kept = __ballot_sync(kFull, gv > kLow && ahead < a.o.top_groups) & a.leaders;
-            if (__any_sync(kFull, unsure && gv > kLow)) {
+            const bool keep = ahead < a.o.top_groups && gv > kLow;
+            kept = __ballot_sync(kFull, keep) & a.leaders;
+            // the last kept group against the best of the others
+            const float lo = -warp_max(keep ? -gv : kMasked), hi = warp_max(keep ? kMasked : gv);
+            const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
+            if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err)))
                 kept = kept_groups64(a, row, wm, LG, lane);
+            if (a.direct) {
+                best4<VPT>(v, x);
+                if (!((kept >> (my_group * LG & 31)) & 1u)) x[0] = x[1] = x[2] = x[3] = kMasked;
+            } else {
+                // the kept groups' experts in a row, 32 at a time
+                put();
+                if ((kept >> lane) & 1u) wm.first[__popc(kept & ((1u << lane) - 1u))] = my_group * per;
                 __syncwarp();
-                put();  // it took the values' room
-            }
-            // the kept groups' experts in a row, 32 at a time
-            if ((kept >> lane) & 1u) wm.first[__popc(kept & ((1u << lane) - 1u))] = my_group * per;
-            __syncwarp();
-            const int count = __popc(kept) * per;
-            held = (count + 31) >> 5;
+                const int count = __popc(kept) * per;
+                held = (count + 31) >> 5;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (i < held) {
-                    const int q = lane + 32 * i, g = q * a.per_inv >> 16;
-                    float y = kMasked;
-                    if (q < count) y = tagged(all[wm.first[g] + q - g * per], i);
-                    insert4(x, y);
-                }
+                for (int i = 0; i < VPT; ++i)
+                    if (i < held) {
+                        const int q = lane + 32 * i, g = q * a.per_inv >> 16;
+                        float y = kMasked;
+                        if (q < count) y = tagged(all[wm.first[g] + q - g * per], i);
+                        insert4(x, y);
+                    }
+            }
         } else {
             best4<VPT>(v, x);
         }
 
-        // the k + 1 best in descending order
+        // the k + 1 best in descending order, the r-th in lane r
         __syncwarp();  // the last token's readers are done
-        float best = kMasked;
+        float best = kMasked, mine = kMasked;
         int taken = 0;
-#pragma unroll 3
-        for (int r = 0; r <= k; ++r) {
+#pragma unroll
+        for (int r = 0; r <= kMaxK; ++r) {
+            if (r > k) break;
             best = warp_max(x[0]);
             const bool own = x[0] == best;
-            if (own) wm.sorted[r] = Cand{best, lane};
+            if (own) wm.place[r] = lane;
+            if (lane == r) mine = best;
             x[0] = own ? x[1] : x[0];
             x[1] = own ? x[2] : x[1];
             x[2] = own ? x[3] : x[2];
@@ -526,31 +552,36 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
             ranked = true;
         }
         __syncwarp();
-        if (lane < k && lane + 1 < n) {
-            const float y0 = wm.sorted[lane].v, y1 = wm.sorted[lane + 1].v;
-            close |= !(y0 - y1 > abs_err + rel_err * (fabsf(y0) + fabsf(y1)) + 1e-37f);
-        }
-        if (__any_sync(kFull, close)) {
-            if (!ranked) rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
-            ranked = true;
-            __syncwarp();
-            sort_candidates64(a, row, wm, n, lane);
-        }
-        const bool live = lane < k && lane < n;
         int e = -1;
-        if (live) {
-            const Cand c = wm.sorted[lane];
-            e = c.e;
-            if (!ranked) {  // the value's lane; its low bits: the register
-                const int j = (int)(__float_as_uint(c.v) & 7u);
-                if (grouped) {
-                    const int q = e + 32 * j, g = q * a.per_inv >> 16;
-                    e = wm.first[g] + q - g * per;
-                } else {
-                    e = e * VPT + j;
-                }
+        const bool live = lane < k && lane < n;
+        if (ranked) {
+            if (lane <= k && lane < n) {
+                mine = wm.sorted[lane].v;
+                e = wm.sorted[lane].e;
+            }
+        } else if (lane < k) {  // the value's lane; its low bits: the register
+            const int j = (int)(__float_as_uint(mine) & 7u), from = wm.place[lane];
+            if (grouped && !a.direct) {
+                const int q = from + 32 * j, g = q * a.per_inv >> 16;
+                e = wm.first[g] + q - g * per;
+            } else {
+                e = from * VPT + j;
             }
         }
+        const float next = __shfl_down_sync(kFull, mine, 1);
+        const bool unclear = live && lane + 1 < n && !(mine - next > abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f);
+        const unsigned pairs = __ballot_sync(kFull, unclear);
+        if (pairs || __any_sync(kFull, close)) {
+            if (((pairs >> (k - 1)) & 1u) || __any_sync(kFull, close)) {  // who is among the k, too
+                if (!ranked) rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
+                __syncwarp();
+                sort_candidates64(a, row, wm, n, lane);
+                e = live ? wm.place[lane] : -1;
+            } else {
+                e = reorder64(a, row, wm, e, k < n ? k : n, lane);
+            }
+        }
+        if (!live) e = -1;
         const float z = live ? row[e] : 0.0f;
         float wt;
         if (a.o.renormalize)
@@ -856,8 +887,11 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
         while (2 * lanes * o.groups <= 32) lanes *= 2;
     unsigned leaders = 0u;
     for (int g = 0; g < o.groups; ++g) leaders |= 1u << (g * lanes);
-    const RouteArgs a{logits, bias, T,      E,      k, per, (65536 + per - 1) / per, lanes, leaders, o, idx, w,
-                      counts, status};
+    // Kept groups that fill at least 16 lanes are taken where they are: the
+    // best k + 1 then ask a lane of 8 experts for a fifth in 0.2% of the tokens.
+    const bool direct = lanes * vpt == per && (vpt <= 4 || o.top_groups * lanes >= 16);
+    const RouteArgs a{logits, bias,   T,      E, k, per, (65536 + per - 1) / per, lanes,
+                      direct, leaders, o, idx, w, counts, status};
     switch (vpt) {
         case 1: return launch_route_v<1>(a, num_sms, st);
         case 2: return launch_route_v<2>(a, num_sms, st);
