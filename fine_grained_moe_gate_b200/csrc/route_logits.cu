@@ -43,11 +43,6 @@ __device__ __forceinline__ int ld_cluster_i32(uint32_t cluster_addr) {
 // Programmatic dependent launch: waits until the kernel before this one on
 // the stream is complete and its writes are visible.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
@@ -111,19 +106,22 @@ struct RouteArgs {
 struct Softmax64 {
     double m, den;
 };
-__device__ Softmax64 softmax64(const float* row, int E, int lane) {
-    double m = neg_inf64();
-    for (int e = lane; e < E; e += 32) {
-        const float z = row[e];
-        if (z == z) m = fmax(m, (double)z);
+__device__ __forceinline__ Softmax64 softmax64(const float* row, int E, int lane) {
+    constexpr int N = kMaxExperts / 32;
+    float z[N], m = neg_inf();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        z[j] = lane + 32 * j < E ? row[lane + 32 * j] : neg_inf();
+        m = fmaxf(m, z[j]);  // NaN drops out
     }
     m = warp_max(m);
     double part = 0.0;
-    for (int e = lane; e < E; e += 32) {
-        const double z = (double)row[e];
-        if (z == z && z != neg_inf64()) part += z == m ? 1.0 : exp(z - m);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {  // side by side: one after the other they took 2 us
+        const double y = exp((double)z[j] - (double)m);
+        part += z[j] == m ? 1.0 : z[j] > neg_inf() ? y : 0.0;
     }
-    return {m, warp_sum(part)};
+    return {(double)m, warp_sum(part)};
 }
 // v of one expert; -inf where it is masked
 __device__ __forceinline__ double value64(const RouteArgs& a, const float* row, int e, const Softmax64& sm) {
@@ -134,29 +132,38 @@ __device__ __forceinline__ double value64(const RouteArgs& a, const float* row, 
     return v == v ? v : neg_inf64();
 }
 
-// Kept groups from 64-bit values: bit g LG for group g.
-__device__ __noinline__ unsigned kept_groups64(const RouteArgs& a, const float* row, WarpMem& wm, int LG, int lane) {
+// Kept groups from 64-bit values (bit g LG for group g): of each group, the
+// values that may be among its group_top largest are evaluated.  all: the
+// 32-bit values; cut: this lane's group's group_top-th, less the error bound.
+__device__ __noinline__ unsigned kept_groups64(const RouteArgs& a, const float* row, const float* all, float cut,
+                                               int lane) {
     const Softmax64 sm = a.o.softmax ? softmax64(row, a.E, lane) : Softmax64{0.0, 1.0};
-    for (int e = lane; e < a.E; e += 32) wm.d[e] = value64(a, row, e, sm);
-    __syncwarp();
-    const int per = a.E / a.o.groups, my = lane / LG;
-    const bool real = my < a.o.groups && my * LG == lane;
-    double gv = neg_inf64();
-    if (real) {
-        double x1 = neg_inf64(), x2 = neg_inf64();
-        for (int i = 0; i < per; ++i) {
-            const double x = wm.d[my * per + i];
+    const int LG = a.group_lanes, my = lane / LG;
+    const int last = my < a.o.groups ? (my + 1) * a.per : 0;
+    double x1 = neg_inf64(), x2 = neg_inf64();
+    int i = my * a.per + (lane & (LG - 1));
+    for (;;) {  // every lane's next value above its cut, evaluated together
+        while (i < last && !(all[i] >= cut)) i += LG;
+        if (!__any_sync(kFull, i < last)) break;
+        if (i < last) {
+            const double x = value64(a, row, i, sm);
             x2 = fmax(x2, fmin(x1, x));
             x1 = fmax(x1, x);
+            i += LG;
         }
-        gv = a.o.group_top == 2 && x2 != neg_inf64() ? x1 + x2 : x1;
     }
+    for (int o = 1; o < LG; o <<= 1) {
+        const double y1 = __shfl_xor_sync(kFull, x1, o), y2 = __shfl_xor_sync(kFull, x2, o);
+        x2 = fmax(fmin(x1, y1), fmax(x2, y2));
+        x1 = fmax(x1, y1);
+    }
+    const double gv = a.o.group_top == 2 && x2 != neg_inf64() ? x1 + x2 : x1;
     int ahead = 0;
     for (int g = 0; g < a.o.groups; ++g) {
         const double x = __shfl_sync(kFull, gv, g * LG);
         ahead += x > gv || (x == gv && g < my);
     }
-    return __ballot_sync(kFull, real && ahead < a.o.top_groups);
+    return __ballot_sync(kFull, gv != neg_inf64() && ahead < a.o.top_groups) & a.leaders;
 }
 
 // The k best of the n candidates by their 64-bit values, ties to the lower expert.
@@ -261,14 +268,15 @@ __device__ __forceinline__ void sort4(float (&x)[4]) {
     order(x[1], x[3]);
     order(x[1], x[2]);
 }
-// The four largest so far, descending, with y among them.
-__device__ __forceinline__ void insert4(float (&x)[4], float y) {
+// The four largest so far, descending, and the fifth, with y among them.
+__device__ __forceinline__ void insert4(float (&x)[4], float& fifth, float y) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) order(x[i], y);
+    fifth = fmaxf(fifth, y);
 }
-// The four largest of v, descending.
+// The four largest of v, descending, and the fifth.
 template <int VPT>
-__device__ __forceinline__ void best4(const float (&v)[VPT], float (&x)[4]) {
+__device__ __forceinline__ void best4(const float (&v)[VPT], float (&x)[4], float& fifth) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = i < VPT ? v[i < VPT ? i : 0] : kMasked;
     if (VPT == 2) order(x[0], x[1]);
@@ -277,7 +285,8 @@ __device__ __forceinline__ void best4(const float (&v)[VPT], float (&x)[4]) {
         float y[4] = {v[4 % VPT], v[5 % VPT], v[6 % VPT], v[7 % VPT]};
         sort4(y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fmaxf(x[i], y[3 - i]);  // the four largest, rising then falling
+        for (int i = 0; i < 4; ++i) order(x[i], y[3 - i]);  // x: the four largest, rising then falling
+        fifth = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
         order(x[0], x[2]);
         order(x[1], x[3]);
         order(x[0], x[1]);
@@ -366,9 +375,11 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     extern __shared__ __align__(16) uint8_t smem[];
     WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
     int* hist = reinterpret_cast<int*>(smem + WARPS * sizeof(WarpMem));
+    int* taken_tokens = hist + kMaxExperts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int E = a.E, k = a.k, e0 = lane * VPT;
     for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
+    if (tid == 0) *taken_tokens = WARPS;
     __syncthreads();
 
     const bool vec = (E & 3) == 0;
@@ -394,7 +405,15 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     const int my_group = lane / LG, sub = lane & (LG - 1);
     const bool real = my_group < a.o.groups;
 
-    for (int t = SMALL ? warp * gridDim.x + blockIdx.x : blockIdx.x * WARPS + warp; t < a.T; t += gridDim.x * WARPS) {
+    // The CTA's warps take its tokens (every gridDim.x-th) as they come free: a
+    // token that needs 64 bits then holds up one warp alone.
+    int t_next;
+    for (int t = warp * gridDim.x + blockIdx.x; t < a.T; t = t_next) {
+        int i_next = 0;
+        if (lane == 0) i_next = atomicAdd(taken_tokens, 1);
+        t_next = (int)min((long long)__shfl_sync(kFull, i_next, 0) * gridDim.x + blockIdx.x, (long long)a.T);
+        if (t_next < a.T && 32 * lane < E)  // its row, on the way while this one is worked on
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(a.logits + (size_t)t_next * E + 32 * lane));
         const float* row = a.logits + (size_t)t * E;
         float v[VPT];
         load_row<VPT>(row, e0, E, vec, kMasked, v);
@@ -450,9 +469,8 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
                 if ((masked >> j) & 1u) v[j] = kMasked;
         const float abs_err = a.bias ? top * kAbsErr : 0.0f, rel_err = a.bias ? kSumErr : kRelErr;
 
-        float x[4] = {kMasked, kMasked, kMasked, kMasked};
+        float x[4] = {kMasked, kMasked, kMasked, kMasked}, fifth = kMasked;
         unsigned kept = a.leaders;
-        int held = VPT;  // values that went into x
         if (grouped) {
             float* all = reinterpret_cast<float*>(wm.d);
             const auto put = [&] {  // the row's values where every lane can read them
@@ -502,29 +520,31 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
             // the last kept group against the best of the others
             const float lo = -warp_max(keep ? -gv : kMasked), hi = warp_max(keep ? kMasked : gv);
             const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
-            if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err)))
-                kept = kept_groups64(a, row, wm, LG, lane);
+            if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err))) {
+                if (in_lanes) put();
+                const float nth = a.o.group_top == 2 && x2 > kLow ? x2 : x1;
+                kept = kept_groups64(a, row, all, cut_of(nth, abs_err, rel_err), lane);
+            }
             if (a.direct) {
-                best4<VPT>(v, x);
-                if (!((kept >> (my_group * LG & 31)) & 1u)) x[0] = x[1] = x[2] = x[3] = kMasked;
+                best4<VPT>(v, x, fifth);
+                if (!((kept >> (my_group * LG & 31)) & 1u)) x[0] = x[1] = x[2] = x[3] = fifth = kMasked;
             } else {
                 // the kept groups' experts in a row, 32 at a time
-                put();
+                if (in_lanes) put();
                 if ((kept >> lane) & 1u) wm.first[__popc(kept & ((1u << lane) - 1u))] = my_group * per;
                 __syncwarp();
                 const int count = __popc(kept) * per;
-                held = (count + 31) >> 5;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
-                    if (i < held) {
+                    if (32 * i < count) {
                         const int q = lane + 32 * i, g = q * a.per_inv >> 16;
                         float y = kMasked;
                         if (q < count) y = tagged(all[wm.first[g] + q - g * per], i);
-                        insert4(x, y);
+                        insert4(x, fifth, y);
                     }
             }
         } else {
-            best4<VPT>(v, x);
+            best4<VPT>(v, x, fifth);
         }
 
         // the k + 1 best in descending order, the r-th in lane r
@@ -547,7 +567,7 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
         // every round one lane's, and no lane's fifth wanted
         bool close = false, ranked = false;
         int n = k + 1;
-        if (__reduce_add_sync(kFull, held > 4 && taken >= 4 ? 1000 : taken) != k + 1 || !(best > kLow)) {
+        if (__reduce_add_sync(kFull, taken >= 4 && fifth >= best ? 1000 : taken) != k + 1 || !(best > kLow)) {
             close = rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
             ranked = true;
         }
@@ -815,7 +835,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_chosen_kernel
 template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
 cudaError_t launch_route(const RouteArgs& a, int grid, cudaStream_t st) {
     auto kern = route_logits_kernel<VPT, SOFTMAX, WARPS, SMALL>;
-    constexpr size_t smem = WARPS * sizeof(WarpMem) + kMaxExperts * sizeof(int);
+    constexpr size_t smem = WARPS * sizeof(WarpMem) + (kMaxExperts + 4) * sizeof(int);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[1];
