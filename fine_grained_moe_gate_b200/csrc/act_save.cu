@@ -8,14 +8,16 @@
 //   routed: dw[q] = sum_i u_i h_i  (h unrounded), wt = w[q], q = perm[r].
 //
 // HBM bound: per element 2 codes + 2/32 scale bytes and 4 of u in, 4 of dadg
-// and 2 of h out.  65536 rows of 2048: 251 us, 6.4 TB/s, the rate of a plain
-// copy.  That takes four chunks of a row in flight per lane, streaming loads
-// and stores, and 4 warps per CTA (8 warps: 258 us, two chunks: 260-291, one:
-// 267-276, plain loads and stores: 256-263).
+// and 2 of h out.  65536 rows of 2048: 242 us, 6.7 TB/s, above the rate of a
+// plain copy.  That takes four chunks of a row in flight per lane, streaming
+// loads and stores, 4 warps per CTA (8 warps: 246 us, two chunks: 252) and the
+// hardware's exponential (250 with expf; with it, plain loads and stores took
+// 5 us more, one chunk 15 more).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.h"
 
 namespace moe {
 namespace {
@@ -68,6 +70,7 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_bwd_saved_kernel(const __g
     const long long r = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (r >= p.rows) return;  // warp-uniform
     const int n = p.n;
+    grid_dependency_wait();
     const long long pr = p.prow ? p.prow[r] : r;
     if (p.prow && (pr < 0 || pr >= p.prow_rows)) {  // warp-uniform
         if (lane == 0) report(p.status, kStDeviceCheck);
@@ -103,14 +106,19 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_bwd_saved_kernel(const __g
             float da[8], dg[8], h[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                // s and 1 - s from e^-|a|, exact to the ends of the range
-                const float t = expf(-fabsf(a[j])), y = __fdividef(1.0f, 1.0f + t), ty = t * y;
+                // s and 1 - s from t = e^-|a|: exact to the ends of the range (t may be subnormal, 1 + t is in
+                // [1, 2]).  The hardware's exponential is off by |a| + 4 units of 2^-24, far below bf16's rounding,
+                // and dw sums n of them.
+                float t, y;
+                asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(fabsf(a[j]) * -1.4426950408889634f));
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + t));
+                const float ty = t * y;
                 const float s = a[j] >= 0.0f ? y : ty, s1 = a[j] >= 0.0f ? ty : y;
                 const float as = a[j] * s;
                 h[j] = as * g[j];
                 dot = fmaf(uv[j], h[j], dot);
                 const float dh = wt * uv[j];
-                da[j] = dh * g[j] * s * fmaf(a[j], s1, 1.0f);
+                da[j] = dh * g[j] * fmaf(as, s1, s);  // g s (1 + a (1 - s))
                 dg[j] = dh * as;
             }
             if (q < 0)  // a row without an assignment: zeros, whatever it holds
@@ -137,9 +145,8 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_bwd_saved_kernel(const __g
 cudaError_t launch_swiglu_bwd_saved(const SwigluBwdSaved& p, cudaStream_t st) {
     if (p.rows <= 0) return cudaSuccess;
     const long long blocks = (p.rows + kWarps - 1) / kWarps;
-    swiglu_bwd_saved_kernel<4><<<(unsigned)blocks, kWarps * 32, 0, st>>>(p);
     note_launches(1);
-    return cudaGetLastError();
+    return launch_after(swiglu_bwd_saved_kernel<4>, dim3((unsigned)blocks), kWarps * 32, 0, 1, st, p);
 }
 
 }  // namespace moe

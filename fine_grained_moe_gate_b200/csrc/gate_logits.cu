@@ -15,6 +15,7 @@
 // store).
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.h"
 #include "tmap.h"
 
 #include <atomic>
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
+    grid_dependency_wait();
     // both CTAs' parts for a pair; rows of the A tile that no box fills only reach TMEM lanes that are not stored
     const uint32_t stage_tx = (uint32_t)(PAIR ? 2 : 1) * (uint32_t)((p.x_rows + n_rows) * BK * 2);
 
@@ -295,21 +297,8 @@ cudaError_t launch_c(const CUtensorMap& tx, const CUtensorMap& tw, const GatePar
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_LIMIT);
     if (err != cudaSuccess) return err;
     constexpr int CL = PAIR ? 2 * C : C;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * CL), (unsigned)chunks);
-    cfg.blockDim = dim3(n_threads<PAIR>());
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kern, tx, tw, p);
     note_launches(1);
-    return err == cudaSuccess ? cudaGetLastError() : err;
+    return launch_after(kern, dim3((unsigned)(tiles * CL), (unsigned)chunks), n_threads<PAIR>(), smem, CL, st, tx, tw, p);
 }
 
 // Clusters of `size` CTAs (1, 2, 4 or 8; one CTA per SM) resident at once on

@@ -20,6 +20,7 @@
 //   dense part:    sigmoid  dz = ds s (1 - s),  softmax  dz = s (ds - sum ds s).
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.h"
 
 namespace moe {
 namespace {
@@ -40,9 +41,6 @@ __device__ __forceinline__ int ld_cluster_i32(uint32_t cluster_addr) {
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
     return v;
 }
-// Programmatic dependent launch: waits until the kernel before this one on
-// the stream is complete and its writes are visible.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename T>
 __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
@@ -378,6 +376,7 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     int* taken_tokens = hist + kMaxExperts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int E = a.E, k = a.k, e0 = lane * VPT;
+    if (SMALL) grid_dependency_wait();
     for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
     if (tid == 0) *taken_tokens = WARPS;
     __syncthreads();
@@ -635,10 +634,11 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     }
 }
 
-// Clears the counters.  The routing kernel may start beside it (it waits for
-// this kernel's end before it adds).
+// Clears the counters.  The routing kernel starts beside it, once everything
+// before both is complete, and waits for this kernel's end before it adds.
 __global__ void clear_counts_kernel(int32_t* counts, int E) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_dependency_wait();
+    grid_launch_dependents();
     for (int e = threadIdx.x; e < E; e += blockDim.x) counts[e] = 0;
 }
 
@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_kernel(const 
     if (t >= a.T) return;  // warp-uniform
     const int E = a.E, k = a.k, e0 = lane * VPT;
     const bool vec = (E & 3) == 0, softmax = a.o.softmax;
+    grid_dependency_wait();
     const float* row = a.logits + (size_t)t * E;
     float* add = rows[warp];  // what the chosen slots add: to dz, or to ds (softmax as scored)
 
@@ -784,6 +785,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_chosen_kernel
     const bool softmax = a.o.softmax;
     int e = -1;
     float G = 0.0f, z = neg_inf();
+    grid_dependency_wait();
     if (slot < k && t < a.T) {
         e = a.idx[(size_t)t * k + slot];
         G = a.dw[(size_t)t * k + slot];
@@ -838,26 +840,8 @@ cudaError_t launch_route(const RouteArgs& a, int grid, cudaStream_t st) {
     constexpr size_t smem = WARPS * sizeof(WarpMem) + (kMaxExperts + 4) * sizeof(int);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    cudaLaunchAttribute attr[1];
-    if (SMALL) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)grid;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-    } else {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(WARPS * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kern, a);
     note_launches(1);
-    return err == cudaSuccess ? cudaGetLastError() : err;
+    return launch_after(kern, dim3((unsigned)grid), WARPS * 32, smem, SMALL ? grid : 1, st, a);
 }
 
 template <int VPT>
@@ -871,9 +855,8 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
         return a.o.softmax ? launch_route<VPT, true, kSmallWarps, true>(a, grid, st)
                            : launch_route<VPT, false, kSmallWarps, true>(a, grid, st);
     }
-    clear_counts_kernel<<<1, 256, 0, st>>>(a.counts, a.E);
     note_launches(1);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);
     if (err != cudaSuccess) return err;
     const int blocks = (a.T + 7) / 8, grid = blocks < 4 * num_sms ? blocks : 4 * num_sms;
     return a.o.softmax ? launch_route<VPT, true, 8, false>(a, grid, st) : launch_route<VPT, false, 8, false>(a, grid, st);
@@ -882,17 +865,16 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
 template <int VPT>
 cudaError_t launch_bwd_v(const RouteBwdArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kBwdWarps - 1) / kBwdWarps);
-    route_logits_bwd_kernel<VPT><<<grid, kBwdWarps * 32, 0, st>>>(a);
     note_launches(1);
-    return cudaGetLastError();
+    return launch_after(route_logits_bwd_kernel<VPT>, dim3(grid), kBwdWarps * 32, 0, 1, st, a);
 }
 
 template <int SLOTS>
 cudaError_t launch_bwd_chosen(const RouteBwdArgs& a, cudaStream_t st) {
     constexpr int per_cta = kBwdWarps * 32 / SLOTS;
-    route_logits_bwd_chosen_kernel<SLOTS><<<(unsigned)((a.T + per_cta - 1) / per_cta), kBwdWarps * 32, 0, st>>>(a);
     note_launches(1);
-    return cudaGetLastError();
+    return launch_after(route_logits_bwd_chosen_kernel<SLOTS>, dim3((unsigned)((a.T + per_cta - 1) / per_cta)),
+                        kBwdWarps * 32, 0, 1, st, a);
 }
 
 }  // namespace
