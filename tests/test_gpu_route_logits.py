@@ -244,6 +244,10 @@ def test_route_agrees_with_moe_route():
 @pytest.mark.parametrize("T,d,E,dtype", [(1, 64, 8, "bf16"), (5, 128, 17, "bf16"), (64, 7168, 256, "bf16"),
                                          (130, 192, 60, "bf16"), (300, 2048, 64, "bf16"), (1000, 512, 255, "bf16"),
                                          (5000, 1024, 250, "bf16"), (20000, 256, 256, "bf16"), (700, 7168, 64, "bf16"),
+                                         (127, 320, 31, "bf16"), (129, 448, 129, "bf16"), (256, 64, 256, "bf16"),
+                                         (2368, 512, 256, "bf16"), (2369, 512, 256, "bf16"), (3001, 1344, 200, "bf16"),
+                                         (4096, 576, 256, "bf16"), (6143, 320, 33, "bf16"), (9473, 192, 256, "bf16"),
+                                         (40000, 128, 16, "bf16"),
                                          (1, 8, 1, "f32"), (33, 40, 5, "f32"), (128, 256, 256, "f32"),
                                          (257, 72, 100, "f32")])
 def test_gate_logits_exact_on_a_grid(T, d, E, dtype):
