@@ -109,8 +109,21 @@ class MoESavedActs(ctypes.Structure):
 
 def saved_acts(t: dict) -> MoESavedActs:
     """MoESavedActs from a dict of device tensors under its field names (the
-    layout of ``saved_act_buffers``).  The tensors must outlive its use."""
-    return MoESavedActs(*[_p(t.get(n)) for n, _ in MoESavedActs._fields_])
+    layout of ``saved_act_buffers``), or of raw pointers.  It keeps the tensors;
+    each call it is passed to checks that they are large enough for its shape."""
+    out, device = MoESavedActs(*[_p(t.get(n)) for n, _ in MoESavedActs._fields_]), None
+    out.tensors, out.sizes = dict(t), {}
+    for n, _ in MoESavedActs._fields_:
+        v = t.get(n)
+        if v is None or isinstance(v, int):
+            continue
+        if not v.is_contiguous():
+            raise MoEError(1, f"saved_acts: {n} must be contiguous, got strides {v.stride()}")
+        if device is not None and device != v.get_device():
+            raise MoEError(1, f"saved_acts: {n} must be on one device with the others, got {v.device}")
+        device, out.sizes[n] = v.get_device(), _nbytes(v)
+    out.device = device  # -1: the CPU, which the calls refuse
+    return out
 
 
 _lib = None
@@ -252,6 +265,28 @@ def _call(name, stream, *args):
     else:
         with torch.cuda.device(dev):
             _check(fn(*out, _stream(stream, dev)), name)
+
+
+def _saved_ref(name, saved, shape, sets, device=-1):
+    """Pointer to ``saved``, whose tensors of the expert sets ("" routed, "s"
+    shared) hold the shape's rows, on the call's device."""
+    if saved is None:
+        return None
+    sizes = getattr(saved, "sizes", None)
+    if sizes:
+        for pre in sets:
+            rows, n = (shape.T * shape.k, shape.I) if pre == "" else (shape.T, shape.S * shape.Is)
+            for f, need in ((pre + "a", rows * n), (pre + "a_scale", rows * n // 32), (pre + "g", rows * n),
+                            (pre + "g_scale", rows * n // 32)):
+                if sizes.get(f, need) < need:
+                    raise MoEError(1, f"{name}: saved {f} needs {need} bytes, has {sizes[f]}")
+        if saved.device < 0 or 0 <= device != saved.device:
+            raise MoEError(1, f"{name}: saved activations must be on the CUDA device of the other tensors")
+    return ctypes.byref(saved)
+
+
+def _device(t) -> int:
+    return -1 if t is None or isinstance(t, int) else t.get_device()
 
 
 def _dt(shape) -> str:
@@ -522,13 +557,15 @@ def moe_ffn_up_save(x_perm, offsets, w1, w3, x, ws1, ws3, shape, h, hs, saved, s
     R, I = T * shape.k, shape.I
     _call("moe_ffn_up_save", stream, ("x_perm", x_perm, dt, R * d), ("offsets", offsets, "int32", E + 1),
           ("w1", w1, dt, E * I * d), ("w3", w3, dt, E * I * d), ("x", x, dt, T * d), ("ws1", ws1, dt, SI * d),
-          ("ws3", ws3, dt, SI * d), shape, ("h", h, dt, R * I), ("hs", hs, dt, T * SI), ctypes.byref(saved))
+          ("ws3", ws3, dt, SI * d), shape, ("h", h, dt, R * I), ("hs", hs, dt, T * SI),
+          _saved_ref("moe_ffn_up_save", saved, shape, ("",) if x is None or SI == 0 else ("", "s"), _device(x_perm)))
 
 
 def moe_swiglu_backward_saved(saved, shape, expert_set, u, perm_tok, topk_w, dadg, h, dw, stream=None):
     R = shape.T * shape.k
     n = R * shape.I if expert_set == MOE_ROUTED else shape.T * shape.S * shape.Is
-    _call("moe_swiglu_backward_saved", stream, ctypes.byref(saved), shape, expert_set, ("u", u, "float32", n),
+    ref = _saved_ref("moe_swiglu_backward_saved", saved, shape, ("",) if expert_set == MOE_ROUTED else ("s",), _device(u))
+    _call("moe_swiglu_backward_saved", stream, ref, shape, expert_set, ("u", u, "float32", n),
           ("perm_tok", perm_tok, "int32", R), ("topk_w", topk_w, "float32", R), ("dadg", dadg, "bfloat16", 2 * n),
           ("h", h, "bfloat16", n), ("dw", dw, "float32", R))
 
@@ -544,10 +581,6 @@ def _layer_args(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape):
                 ws3=("ws3", ws3, dt, SI * d), ws2=("ws2", ws2, dt, SI * d))
 
 
-def _saved_ref(saved):
-    return None if saved is None else ctypes.byref(saved)
-
-
 def moe_layer_forward_logits(x, w_gate, bias, w1, w3, w2, ws1, ws3, ws2, shape, opts, y, logits, topk_idx, topk_w,
                              counts, saved, workspace, stream=None):
     T, E, k = shape.T, shape.E, shape.k
@@ -555,7 +588,8 @@ def moe_layer_forward_logits(x, w_gate, bias, w1, w3, w2, ws1, ws3, ws2, shape, 
     _call("moe_layer_forward_logits", stream, a["x"], a["w_gate"], ("bias", bias, "float32", E), a["w1"], a["w3"],
           a["w2"], a["ws1"], a["ws3"], a["ws2"], shape, opts, ("y", y, _dt(shape), T * shape.d),
           ("logits", logits, "float32", T * E), ("topk_idx", topk_idx, "int32", T * k),
-          ("topk_w", topk_w, "float32", T * k), ("counts", counts, "int32", E), _saved_ref(saved),
+          ("topk_w", topk_w, "float32", T * k), ("counts", counts, "int32", E),
+          _saved_ref("moe_layer_forward_logits", saved, shape, ("", "s") if shape.S > 0 else ("",), _device(x)),
           ("workspace", workspace, "uint8", 0), _nbytes(workspace))
 
 
@@ -571,7 +605,8 @@ def moe_layer_backward_logits(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape, opts,
     f = lambda name, t, n: (name, t, "float32", n)
     a = _layer_args(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape)
     _call("moe_layer_backward_logits", stream, a["x"], a["w_gate"], a["w1"], a["w3"], a["w2"], a["ws1"], a["ws3"],
-          a["ws2"], shape, opts, _saved_ref(saved), f("logits", logits, T * E), ("topk_idx", topk_idx, "int32", T * k),
+          a["ws2"], shape, opts,
+          _saved_ref("moe_layer_backward_logits", saved, shape, ("", "s") if shape.S > 0 else ("",), _device(x)), f("logits", logits, T * E), ("topk_idx", topk_idx, "int32", T * k),
           f("topk_w", topk_w, T * k), ("counts", counts, "int32", E), f("dscores", dscores, T * E), f("dy", dy, T * d),
           float(alpha), int(seq_len), f("dx", dx, T * d), f("dw_gate", dw_gate, E * d), f("dw1", dw1, EId),
           f("dw3", dw3, EId), f("dw2", dw2, EId), f("dws1", dws1, SI * d), f("dws3", dws3, SI * d),

@@ -232,6 +232,8 @@ moe_status do_swiglu(const void* x_perm, const int32_t* offsets, const void* w1,
 // ---- routing from logits, saved activations ----------------------------------
 
 constexpr int kMaxRouteGroups = 32;
+// Token tiles (at most 256) past the last token stay within 32 bits.
+constexpr int kMaxGateTokens = 0x7fffffff - 255;
 
 moe_status validate_opts(const moe_route_opts& o, const moe_shape& sh) {
     if (o.score != MOE_SCORE_SIGMOID && o.score != MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID_ARG;
@@ -241,7 +243,7 @@ moe_status validate_opts(const moe_route_opts& o, const moe_shape& sh) {
     if (o.renormalize != 0 && o.renormalize != 1) return MOE_ERR_INVALID_ARG;
     if ((long long)o.top_groups * (sh.E / o.groups) < sh.k) return MOE_ERR_INVALID_ARG;
     if (!(o.scale - o.scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // NaN or infinite
-    return o.groups > kMaxRouteGroups ? MOE_ERR_UNSUPPORTED : MOE_OK;
+    return o.groups > kMaxRouteGroups || sh.T > kMaxGateTokens ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 moe::RouteOpts route_opts(const moe_route_opts& o) {
@@ -801,6 +803,7 @@ moe_status moe_layer_forward(const void* x, const void* w_gate, const float* bia
 moe_status moe_gate_logits(const void* x, const void* w_gate, moe_shape sh, float* logits, void* stream) {
     moe_status v = validate_shape(sh);
     if (v != MOE_OK) return v;
+    MOE_REQUIRE(sh.T <= kMaxGateTokens, MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE(w_gate, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(sh.T == 0 || (x && logits), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(aligned16(x) && aligned16(w_gate) && aligned16(logits), MOE_ERR_ALIGNMENT);

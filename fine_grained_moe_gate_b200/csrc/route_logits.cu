@@ -858,13 +858,13 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
     note_launches(1);
     const cudaError_t err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);
     if (err != cudaSuccess) return err;
-    const int blocks = (a.T + 7) / 8, grid = blocks < 4 * num_sms ? blocks : 4 * num_sms;
+    const int blocks = (a.T - 1) / 8 + 1, grid = blocks < 4 * num_sms ? blocks : 4 * num_sms;
     return a.o.softmax ? launch_route<VPT, true, 8, false>(a, grid, st) : launch_route<VPT, false, 8, false>(a, grid, st);
 }
 
 template <int VPT>
 cudaError_t launch_bwd_v(const RouteBwdArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)((a.T + kBwdWarps - 1) / kBwdWarps);
+    const unsigned grid = (unsigned)((a.T - 1) / kBwdWarps + 1);
     note_launches(1);
     return launch_after(route_logits_bwd_kernel<VPT>, dim3(grid), kBwdWarps * 32, 0, 1, st, a);
 }
@@ -873,7 +873,7 @@ template <int SLOTS>
 cudaError_t launch_bwd_chosen(const RouteBwdArgs& a, cudaStream_t st) {
     constexpr int per_cta = kBwdWarps * 32 / SLOTS;
     note_launches(1);
-    return launch_after(route_logits_bwd_chosen_kernel<SLOTS>, dim3((unsigned)((a.T + per_cta - 1) / per_cta)),
+    return launch_after(route_logits_bwd_chosen_kernel<SLOTS>, dim3((unsigned)((a.T - 1) / per_cta + 1)),
                         kBwdWarps * 32, 0, 1, st, a);
 }
 

@@ -459,6 +459,7 @@ MOE_API moe_status moe_layer_forward_fp8(const void* x, const void* w_gate, cons
  *               top_groups == groups: no restriction (the values are not used)
  *   renormalize 1: weights divided by the sum over the chosen k;  0: as scored
  *   scale       finite factor on the weights
+ * T is at most 2^31 - 256.  Outputs overlap neither inputs nor each other.
  * -------------------------------------------------------------------------*/
 typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
 typedef struct {
@@ -534,7 +535,7 @@ MOE_API moe_status moe_ffn_up_save(const void* x_perm, const int32_t* offsets, c
  *   h[r] = a s g                                  [rows][n], NULL: not wanted
  * MOE_ROUTED: row r is assignment q = perm_tok[r], wt = topk_w[q], and dw[q]
  *   = sum_i u[r][i] (a s g)[i] (unrounded), the gradient of topk_w for u = dy
- *   W2;  perm_tok [T*k], topk_w [T*k], dw [T*k].  An entry of perm_tok outside
+ *   W2;  perm_tok (moe_permute's) [T*k], topk_w [T*k], dw [T*k].  An entry of perm_tok outside
  *   [0, T*k) is reported (MOE_ERR_DEVICE_CHECK); its row gets zeros.
  * MOE_SHARED: wt = 1; perm_tok, topk_w and dw are ignored (may be NULL).
  * u [rows][n] fp32 (the gradient at h before the weight); dadg, h bf16. */

@@ -225,3 +225,31 @@ def test_binding_refuses_wrong_tensors():
         moe.moe_layer_forward_logits(bf[:5], bf, None, bf, bf, bf, bf, bf, bf, sh, o, bf, z, idx, w, counts, None, bf)
     with pytest.raises(moe.MoEError, match="x must be"):
         moe.moe_layer_backward_logits(bf[:5], *[bf] * 7, sh, o, None, z, idx, w, counts, None, z, 0.0, 0, *[z] * 9, bf)
+
+
+def test_refuses_more_tokens_than_tiles_can_count(L):
+    sh = shape(T=(1 << 31) - 255, E=2, k=1)
+    o = opts(groups=1, top_groups=1)
+    assert _route(L, sh, o) == UNSUPPORTED
+    assert _route_bwd(L, sh, o) == UNSUPPORTED
+    assert L.moe_gate_logits(c(FAKE), c(FAKE), sh, c(FAKE), None) == UNSUPPORTED
+
+
+def test_saved_act_tensors_are_checked():
+    import torch
+    sh = shape()
+    buf = moe.saved_act_buffers(sh, "cpu")
+    with pytest.raises(moe.MoEError, match="device"):
+        moe.moe_swiglu_backward_saved(moe.saved_acts(buf), sh, moe.MOE_ROUTED, FAKE, FAKE, FAKE, FAKE, None, FAKE, stream=0)
+    with pytest.raises(moe.MoEError, match="contiguous"):
+        moe.saved_acts({"a": torch.empty((4, 8), dtype=torch.uint8).t()})
+    s = moe.saved_acts({n: FAKE for n, _ in moe.MoESavedActs._fields_})
+    s.device = 0
+    rows = dict(a=sh.T * sh.k * sh.I, g_scale=sh.T * sh.k * sh.I // 32, sa=sh.T * sh.Is, sg_scale=sh.T * sh.Is // 32)
+    for name, need in rows.items():  # a buffer of one byte less than its rows
+        s.sizes = {name: need - 1}
+        part = moe.MOE_SHARED if name.startswith("s") else moe.MOE_ROUTED
+        with pytest.raises(moe.MoEError, match=name):
+            moe.moe_swiglu_backward_saved(s, sh, part, FAKE, FAKE, FAKE, FAKE, None, FAKE, stream=0)
+        with pytest.raises(moe.MoEError, match=name):
+            moe.moe_ffn_up_save(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, sh, FAKE, FAKE, s, stream=0)
