@@ -22,11 +22,14 @@
 #include "kernels.h"
 #include "pdl.h"
 
+#include <cstddef>
+
 namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxK = 16;
+constexpr int kQuadTokens = 128;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ double neg_inf64() { return __longlong_as_double(0xfff0000000000000ll); }
@@ -92,6 +95,9 @@ struct RouteArgs {
     int group_lanes;   // lanes that take a group's values, a power of two
     int direct;        // the kept groups' values are taken where they are, not listed again
     unsigned leaders;  // lane g group_lanes of every group g
+    // four tokens per warp: runs of experts (the groups, or all as one) in chunks of four
+    int run, run_chunks, chunks;
+    int chunk_inv;     // c / run_chunks = c chunk_inv >> 16
     RouteOpts o;
     int32_t* idx;
     float* w;
@@ -249,9 +255,10 @@ constexpr float kLog2e = 1.4426950408889634f, kFltMax = 3.4028234664e38f;
 // held above it (those beyond -1e37 tie in 32 bits and are compared in 64).
 constexpr float kMasked = -kFltMax, kLow = -1e38f;
 
-// v with its low three bits replaced by j.
+// v with its low bits (three, or those of MASK) replaced by j.
+template <uint32_t MASK = 7u>
 __device__ __forceinline__ float tagged(float v, int j) {
-    return __uint_as_float((__float_as_uint(v) & ~7u) | (uint32_t)j);
+    return __uint_as_float((__float_as_uint(v) & ~MASK) | (uint32_t)j);
 }
 
 __device__ __forceinline__ void order(float& a, float& b) {  // a >= b
@@ -363,28 +370,12 @@ __device__ __noinline__ bool rank_candidates(const RouteArgs& a, const float (&v
     return equal;
 }
 
-// Lane l holds experts [l VPT, (l + 1) VPT).  Grouped choices list the kept
-// groups' experts again over all lanes, so that no lane holds many of them.
-// SMALL: one cluster takes the batch and adds its CTAs' counts itself;
-// otherwise counts were cleared by the kernel before this one on the stream.
-template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
-__global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
-    route_logits_kernel(const __grid_constant__ RouteArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
-    int* hist = reinterpret_cast<int*>(smem + WARPS * sizeof(WarpMem));
-    int* taken_tokens = hist + kMaxExperts;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int E = a.E, k = a.k, e0 = lane * VPT;
-    if (SMALL) grid_dependency_wait();
-    for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
-    if (tid == 0) *taken_tokens = WARPS;
-    __syncthreads();
-
-    const bool vec = (E & 3) == 0;
-    float b[VPT];
-    bool odd = false;  // a bias that masks or forces
-    load_row<VPT>(a.bias ? a.bias : a.logits, e0, a.bias ? E : 0, vec, 0.0f, b);
+// This lane's biases, as the 32-bit choice takes them; odd: one masks or forces.
+template <int VPT>
+__device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&b)[VPT], bool& odd) {
+    const int E = a.E, e0 = lane * VPT;
+    odd = false;
+    load_row<VPT>(a.bias ? a.bias : a.logits, e0, a.bias ? E : 0, (E & 3) == 0, 0.0f, b);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         if (b[j] != b[j]) {  // masked, and reported
@@ -396,6 +387,15 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
         if (e0 + j >= E) b[j] = kMasked;
     }
     odd = __any_sync(kFull, odd);
+}
+
+// One token by one warp.  Lane l holds experts [l VPT, (l + 1) VPT).  Grouped choices list the kept
+// groups' experts again over all lanes, so that no lane holds many of them.
+template <int VPT, bool SOFTMAX>
+__device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int* hist, const float (&b)[VPT], bool odd,
+                                            int t, int lane) {
+    const int E = a.E, k = a.k, e0 = lane * VPT;
+    const bool vec = (E & 3) == 0;
     // Groups: LG lanes take a group's values, from their registers where a
     // group is a power of two of whole lanes, else from shared memory.
     const bool grouped = a.o.top_groups < a.o.groups;
@@ -403,6 +403,230 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     const bool in_lanes = LG * VPT == per;
     const int my_group = lane / LG, sub = lane & (LG - 1);
     const bool real = my_group < a.o.groups;
+            const float* row = a.logits + (size_t)t * E;
+            float v[VPT];
+            load_row<VPT>(row, e0, E, vec, kMasked, v);
+            float nf = 0.0f;  // NaN where a logit is not finite
+    #pragma unroll
+            for (int j = 0; j < VPT; ++j) nf = fmaf(v[j], 0.0f, nf);
+            bool special = nf != nf;
+            float m = 0.0f, top = 1.0f;  // softmax: the largest logit; a bound of the scores
+            if (SOFTMAX) {
+                m = v[0];
+    #pragma unroll
+                for (int j = 1; j < VPT; ++j) m = fmaxf(m, v[j]);  // NaN drops out
+                m = warp_max(m);
+                special |= !(m > kLow);
+            }
+            special = __any_sync(kFull, special) || odd;  // masks, infinities, NaN: the long way
+            bool bad = false;
+            unsigned masked = 0u;
+            if (special) {
+    #pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    bad |= v[j] != v[j];
+                    if (!(v[j] > neg_inf()) || b[j] == neg_inf() || e0 + j >= E) masked |= 1u << j;
+                    if (!(v[j] > neg_inf()) || e0 + j >= E) v[j] = neg_inf();
+                }
+            }
+            if (SOFTMAX) {
+                float part = 0.0f;
+                if (special) {
+                    const float ref = fabsf(m) <= kFltMax ? m : 0.0f;
+    #pragma unroll
+                    for (int j = 0; j < VPT; ++j) {
+                        const float z = v[j];
+                        v[j] = ex2_fast((z - ref) * kLog2e);
+                        if (m > kFltMax) v[j] = z == m ? 1.0f : 0.0f;  // logit +inf
+                    }
+                } else {
+    #pragma unroll
+                    for (int j = 0; j < VPT; ++j) v[j] = ex2_fast((v[j] - m) * kLog2e);
+                }
+    #pragma unroll
+                for (int j = 0; j < VPT; ++j) part += v[j];
+                top = rcp_fast(fmaxf(warp_sum(part), 1e-30f));
+    #pragma unroll
+                for (int j = 0; j < VPT; ++j) v[j] = tagged(fmaf(v[j], top, b[j]), j);
+            } else {
+    #pragma unroll
+                for (int j = 0; j < VPT; ++j) v[j] = tagged(rcp_fast(1.0f + ex2_fast(v[j] * -kLog2e)) + b[j], j);
+            }
+            if (special)
+    #pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if ((masked >> j) & 1u) v[j] = kMasked;
+            const float abs_err = a.bias ? top * kAbsErr : 0.0f, rel_err = a.bias ? kSumErr : kRelErr;
+
+            float x[4] = {kMasked, kMasked, kMasked, kMasked}, fifth = kMasked;
+            unsigned kept = a.leaders;
+            if (grouped) {
+                float* all = reinterpret_cast<float*>(wm.d);
+                const auto put = [&] {  // the row's values where every lane can read them
+                    __syncwarp();
+                    if (VPT % 4 == 0) {
+    #pragma unroll
+                        for (int j = 0; j < VPT; j += 4)
+                            *reinterpret_cast<float4*>(all + e0 + j) =
+                                make_float4(v[j], v[j + 1 < VPT ? j + 1 : j], v[j + 2 < VPT ? j + 2 : j],
+                                            v[j + 3 < VPT ? j + 3 : j]);
+                    } else {
+    #pragma unroll
+                        for (int j = 0; j < VPT; ++j) all[e0 + j] = v[j];
+                    }
+                    __syncwarp();
+                };
+                float x1 = kMasked, x2 = kMasked;
+                if (in_lanes) {
+                    best2<VPT>(v, x1, x2);
+                } else {
+                    put();
+                    if (real) {
+                        const int last = (my_group + 1) * per;
+                        for (int i = my_group * per + sub; i < last; i += LG) {
+                            const float y = all[i];
+                            x2 = fmaxf(x2, fminf(x1, y));
+                            x1 = fmaxf(x1, y);
+                        }
+                    }
+                }
+                for (int o = 1; o < LG; o <<= 1) {
+                    const float y1 = __shfl_xor_sync(kFull, x1, o), y2 = __shfl_xor_sync(kFull, x2, o);
+                    x2 = fmaxf(fminf(x1, y1), fmaxf(x2, y2));
+                    x1 = fmaxf(x1, y1);
+                }
+                float gv = a.o.group_top == 2 && x2 > kLow ? x1 + x2 : x1;
+                if (!real) gv = kMasked;
+                // a group's lanes share the comparison with the others
+                int ahead = 0;
+                for (int i = 0; i < a.o.groups; i += LG) {
+                    const float y = __shfl_sync(kFull, gv, ((i + sub) * LG) & 31);
+                    ahead += i + sub < a.o.groups && y > gv;
+                }
+                for (int o = 1; o < LG; o <<= 1) ahead += __shfl_xor_sync(kFull, ahead, o);
+                const bool keep = ahead < a.o.top_groups && gv > kLow;
+                kept = __ballot_sync(kFull, keep) & a.leaders;
+                // the last kept group against the best of the others
+                const float lo = -warp_max(keep ? -gv : kMasked), hi = warp_max(keep ? kMasked : gv);
+                const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
+                if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err))) {
+                    if (in_lanes) put();
+                    const float nth = a.o.group_top == 2 && x2 > kLow ? x2 : x1;
+                    kept = kept_groups64(a, row, all, cut_of(nth, abs_err, rel_err), lane);
+                }
+                if (a.direct) {
+                    best4<VPT>(v, x, fifth);
+                    if (!((kept >> (my_group * LG & 31)) & 1u)) x[0] = x[1] = x[2] = x[3] = fifth = kMasked;
+                } else {
+                    // the kept groups' experts in a row, 32 at a time
+                    if (in_lanes) put();
+                    if ((kept >> lane) & 1u) wm.first[__popc(kept & ((1u << lane) - 1u))] = my_group * per;
+                    __syncwarp();
+                    const int count = __popc(kept) * per;
+    #pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (32 * i < count) {
+                            const int q = lane + 32 * i, g = q * a.per_inv >> 16;
+                            float y = kMasked;
+                            if (q < count) y = tagged(all[wm.first[g] + q - g * per], i);
+                            insert4(x, fifth, y);
+                        }
+                }
+            } else {
+                best4<VPT>(v, x, fifth);
+            }
+
+            // the k + 1 best in descending order, the r-th in lane r
+            __syncwarp();  // the last token's readers are done
+            float best = kMasked, mine = kMasked;
+            int taken = 0;
+    #pragma unroll
+            for (int r = 0; r <= kMaxK; ++r) {
+                if (r > k) break;
+                best = warp_max(x[0]);
+                const bool own = x[0] == best;
+                if (own) wm.place[r] = lane;
+                if (lane == r) mine = best;
+                x[0] = own ? x[1] : x[0];
+                x[1] = own ? x[2] : x[1];
+                x[2] = own ? x[3] : x[2];
+                x[3] = own ? kMasked : x[3];
+                taken += own;
+            }
+            // every round one lane's, and no lane's fifth wanted
+            bool close = false, ranked = false;
+            int n = k + 1;
+            if (__reduce_add_sync(kFull, taken >= 4 && fifth >= best ? 1000 : taken) != k + 1 || !(best > kLow)) {
+                close = rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
+                ranked = true;
+            }
+            __syncwarp();
+            int e = -1;
+            const bool live = lane < k && lane < n;
+            if (ranked) {
+                if (lane <= k && lane < n) {
+                    mine = wm.sorted[lane].v;
+                    e = wm.sorted[lane].e;
+                }
+            } else if (lane < k) {  // the value's lane; its low bits: the register
+                const int j = (int)(__float_as_uint(mine) & 7u), from = wm.place[lane];
+                if (grouped && !a.direct) {
+                    const int q = from + 32 * j, g = q * a.per_inv >> 16;
+                    e = wm.first[g] + q - g * per;
+                } else {
+                    e = from * VPT + j;
+                }
+            }
+            const float next = __shfl_down_sync(kFull, mine, 1);
+            const bool unclear = live && lane + 1 < n && !(mine - next > abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f);
+            const unsigned pairs = __ballot_sync(kFull, unclear);
+            if (pairs || __any_sync(kFull, close)) {
+                if (((pairs >> (k - 1)) & 1u) || __any_sync(kFull, close)) {  // who is among the k, too
+                    if (!ranked) rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
+                    __syncwarp();
+                    sort_candidates64(a, row, wm, n, lane);
+                    e = live ? wm.place[lane] : -1;
+                } else {
+                    e = reorder64(a, row, wm, e, k < n ? k : n, lane);
+                }
+            }
+            if (!live) e = -1;
+            const float z = live ? row[e] : 0.0f;
+            float wt;
+            if (a.o.renormalize)
+                wt = k <= 8 ? chosen_share<8>(z, live, SOFTMAX) : chosen_share<16>(z, live, SOFTMAX);
+            else
+                wt = !live ? 0.0f : SOFTMAX ? (z == m ? top : expf(z - m) * top) : __fdividef(1.0f, 1.0f + expf(-z));
+            if (lane < k) {
+                a.idx[(size_t)t * k + lane] = e;
+                a.w[(size_t)t * k + lane] = wt * a.o.scale;
+                if (live)
+                    atomicAdd(&hist[e], 1);
+                else
+                    bad = true;
+            }
+            if (bad) report(a.status, kStDeviceCheck);
+}
+
+// SMALL: one cluster takes the batch and adds its CTAs' counts itself;
+// otherwise counts were cleared by the kernel before this one on the stream.
+template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
+__global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
+    route_logits_kernel(const __grid_constant__ RouteArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
+    int* hist = reinterpret_cast<int*>(smem + WARPS * sizeof(WarpMem));
+    int* taken_tokens = hist + kMaxExperts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int E = a.E;
+    if (SMALL) grid_dependency_wait();
+    for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
+    if (tid == 0) *taken_tokens = WARPS;
+    __syncthreads();
+
+    float b[VPT];
+    bool odd;
+    load_bias<VPT>(a, lane, b, odd);
 
     // The CTA's warps take its tokens (every gridDim.x-th) as they come free: a
     // token that needs 64 bits then holds up one warp alone.
@@ -413,209 +637,7 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
         t_next = (int)min((long long)__shfl_sync(kFull, i_next, 0) * gridDim.x + blockIdx.x, (long long)a.T);
         if (t_next < a.T && 32 * lane < E)  // its row, on the way while this one is worked on
             asm volatile("prefetch.global.L1 [%0];" ::"l"(a.logits + (size_t)t_next * E + 32 * lane));
-        const float* row = a.logits + (size_t)t * E;
-        float v[VPT];
-        load_row<VPT>(row, e0, E, vec, kMasked, v);
-        float nf = 0.0f;  // NaN where a logit is not finite
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) nf = fmaf(v[j], 0.0f, nf);
-        bool special = nf != nf;
-        float m = 0.0f, top = 1.0f;  // softmax: the largest logit; a bound of the scores
-        if (SOFTMAX) {
-            m = v[0];
-#pragma unroll
-            for (int j = 1; j < VPT; ++j) m = fmaxf(m, v[j]);  // NaN drops out
-            m = warp_max(m);
-            special |= !(m > kLow);
-        }
-        special = __any_sync(kFull, special) || odd;  // masks, infinities, NaN: the long way
-        bool bad = false;
-        unsigned masked = 0u;
-        if (special) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                bad |= v[j] != v[j];
-                if (!(v[j] > neg_inf()) || b[j] == neg_inf() || e0 + j >= E) masked |= 1u << j;
-                if (!(v[j] > neg_inf()) || e0 + j >= E) v[j] = neg_inf();
-            }
-        }
-        if (SOFTMAX) {
-            float part = 0.0f;
-            if (special) {
-                const float ref = fabsf(m) <= kFltMax ? m : 0.0f;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const float z = v[j];
-                    v[j] = ex2_fast((z - ref) * kLog2e);
-                    if (m > kFltMax) v[j] = z == m ? 1.0f : 0.0f;  // logit +inf
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) v[j] = ex2_fast((v[j] - m) * kLog2e);
-            }
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) part += v[j];
-            top = rcp_fast(fmaxf(warp_sum(part), 1e-30f));
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) v[j] = tagged(fmaf(v[j], top, b[j]), j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) v[j] = tagged(rcp_fast(1.0f + ex2_fast(v[j] * -kLog2e)) + b[j], j);
-        }
-        if (special)
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if ((masked >> j) & 1u) v[j] = kMasked;
-        const float abs_err = a.bias ? top * kAbsErr : 0.0f, rel_err = a.bias ? kSumErr : kRelErr;
-
-        float x[4] = {kMasked, kMasked, kMasked, kMasked}, fifth = kMasked;
-        unsigned kept = a.leaders;
-        if (grouped) {
-            float* all = reinterpret_cast<float*>(wm.d);
-            const auto put = [&] {  // the row's values where every lane can read them
-                __syncwarp();
-                if (VPT % 4 == 0) {
-#pragma unroll
-                    for (int j = 0; j < VPT; j += 4)
-                        *reinterpret_cast<float4*>(all + e0 + j) =
-                            make_float4(v[j], v[j + 1 < VPT ? j + 1 : j], v[j + 2 < VPT ? j + 2 : j],
-                                        v[j + 3 < VPT ? j + 3 : j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VPT; ++j) all[e0 + j] = v[j];
-                }
-                __syncwarp();
-            };
-            float x1 = kMasked, x2 = kMasked;
-            if (in_lanes) {
-                best2<VPT>(v, x1, x2);
-            } else {
-                put();
-                if (real) {
-                    const int last = (my_group + 1) * per;
-                    for (int i = my_group * per + sub; i < last; i += LG) {
-                        const float y = all[i];
-                        x2 = fmaxf(x2, fminf(x1, y));
-                        x1 = fmaxf(x1, y);
-                    }
-                }
-            }
-            for (int o = 1; o < LG; o <<= 1) {
-                const float y1 = __shfl_xor_sync(kFull, x1, o), y2 = __shfl_xor_sync(kFull, x2, o);
-                x2 = fmaxf(fminf(x1, y1), fmaxf(x2, y2));
-                x1 = fmaxf(x1, y1);
-            }
-            float gv = a.o.group_top == 2 && x2 > kLow ? x1 + x2 : x1;
-            if (!real) gv = kMasked;
-            // a group's lanes share the comparison with the others
-            int ahead = 0;
-            for (int i = 0; i < a.o.groups; i += LG) {
-                const float y = __shfl_sync(kFull, gv, ((i + sub) * LG) & 31);
-                ahead += i + sub < a.o.groups && y > gv;
-            }
-            for (int o = 1; o < LG; o <<= 1) ahead += __shfl_xor_sync(kFull, ahead, o);
-            const bool keep = ahead < a.o.top_groups && gv > kLow;
-            kept = __ballot_sync(kFull, keep) & a.leaders;
-            // the last kept group against the best of the others
-            const float lo = -warp_max(keep ? -gv : kMasked), hi = warp_max(keep ? kMasked : gv);
-            const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
-            if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err))) {
-                if (in_lanes) put();
-                const float nth = a.o.group_top == 2 && x2 > kLow ? x2 : x1;
-                kept = kept_groups64(a, row, all, cut_of(nth, abs_err, rel_err), lane);
-            }
-            if (a.direct) {
-                best4<VPT>(v, x, fifth);
-                if (!((kept >> (my_group * LG & 31)) & 1u)) x[0] = x[1] = x[2] = x[3] = fifth = kMasked;
-            } else {
-                // the kept groups' experts in a row, 32 at a time
-                if (in_lanes) put();
-                if ((kept >> lane) & 1u) wm.first[__popc(kept & ((1u << lane) - 1u))] = my_group * per;
-                __syncwarp();
-                const int count = __popc(kept) * per;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    if (32 * i < count) {
-                        const int q = lane + 32 * i, g = q * a.per_inv >> 16;
-                        float y = kMasked;
-                        if (q < count) y = tagged(all[wm.first[g] + q - g * per], i);
-                        insert4(x, fifth, y);
-                    }
-            }
-        } else {
-            best4<VPT>(v, x, fifth);
-        }
-
-        // the k + 1 best in descending order, the r-th in lane r
-        __syncwarp();  // the last token's readers are done
-        float best = kMasked, mine = kMasked;
-        int taken = 0;
-#pragma unroll
-        for (int r = 0; r <= kMaxK; ++r) {
-            if (r > k) break;
-            best = warp_max(x[0]);
-            const bool own = x[0] == best;
-            if (own) wm.place[r] = lane;
-            if (lane == r) mine = best;
-            x[0] = own ? x[1] : x[0];
-            x[1] = own ? x[2] : x[1];
-            x[2] = own ? x[3] : x[2];
-            x[3] = own ? kMasked : x[3];
-            taken += own;
-        }
-        // every round one lane's, and no lane's fifth wanted
-        bool close = false, ranked = false;
-        int n = k + 1;
-        if (__reduce_add_sync(kFull, taken >= 4 && fifth >= best ? 1000 : taken) != k + 1 || !(best > kLow)) {
-            close = rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
-            ranked = true;
-        }
-        __syncwarp();
-        int e = -1;
-        const bool live = lane < k && lane < n;
-        if (ranked) {
-            if (lane <= k && lane < n) {
-                mine = wm.sorted[lane].v;
-                e = wm.sorted[lane].e;
-            }
-        } else if (lane < k) {  // the value's lane; its low bits: the register
-            const int j = (int)(__float_as_uint(mine) & 7u), from = wm.place[lane];
-            if (grouped && !a.direct) {
-                const int q = from + 32 * j, g = q * a.per_inv >> 16;
-                e = wm.first[g] + q - g * per;
-            } else {
-                e = from * VPT + j;
-            }
-        }
-        const float next = __shfl_down_sync(kFull, mine, 1);
-        const bool unclear = live && lane + 1 < n && !(mine - next > abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f);
-        const unsigned pairs = __ballot_sync(kFull, unclear);
-        if (pairs || __any_sync(kFull, close)) {
-            if (((pairs >> (k - 1)) & 1u) || __any_sync(kFull, close)) {  // who is among the k, too
-                if (!ranked) rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
-                __syncwarp();
-                sort_candidates64(a, row, wm, n, lane);
-                e = live ? wm.place[lane] : -1;
-            } else {
-                e = reorder64(a, row, wm, e, k < n ? k : n, lane);
-            }
-        }
-        if (!live) e = -1;
-        const float z = live ? row[e] : 0.0f;
-        float wt;
-        if (a.o.renormalize)
-            wt = k <= 8 ? chosen_share<8>(z, live, SOFTMAX) : chosen_share<16>(z, live, SOFTMAX);
-        else
-            wt = !live ? 0.0f : SOFTMAX ? (z == m ? top : expf(z - m) * top) : __fdividef(1.0f, 1.0f + expf(-z));
-        if (lane < k) {
-            a.idx[(size_t)t * k + lane] = e;
-            a.w[(size_t)t * k + lane] = wt * a.o.scale;
-            if (live)
-                atomicAdd(&hist[e], 1);
-            else
-                bad = true;
-        }
-        if (bad) report(a.status, kStDeviceCheck);
+        route_token<VPT, SOFTMAX>(a, wm, hist, b, odd, t, lane);
     }
     if (SMALL) {
         cluster_sync_all();  // every CTA's counts are in
@@ -632,6 +654,487 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
         for (int e = tid; e < E; e += WARPS * 32)
             if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
     }
+}
+
+// ---- four tokens per warp ----
+
+// v of a sigmoid gate
+__device__ __noinline__ double sigmoid64(float z, float b) { return 1.0 / (1.0 + exp(-(double)z)) + (double)b; }
+
+// One token by one warp with every value in 64 bits: k rounds of the largest.
+// Rarely called, so its instructions come from memory: loops instead of
+// unrolled code (the 32-bit choice with its 64-bit repairs, unrolled, took 5
+// us from a cold start).
+template <bool SOFTMAX>
+__device__ __noinline__ void route_token64(const RouteArgs& a, WarpMem& wm, int* hist, int t, int lane) {
+    constexpr int N = kMaxExperts / 32;
+    const int E = a.E, k = a.k;
+    const float* row = a.logits + (size_t)t * E;
+    __syncwarp();
+    bool bad = false;
+    float m = neg_inf();
+    double den = 1.0;
+    for (int e = lane; e < E; e += 32) {
+        const float z = row[e];
+        bad |= z != z;
+        m = fmaxf(m, z);  // NaN drops out
+    }
+    if (SOFTMAX) {
+        m = warp_max(m);
+        double part = 0.0;
+#pragma unroll 2
+        for (int e = lane; e < E; e += 32) {
+            const float z = row[e];
+            const double y = z == m ? 1.0 : z > neg_inf() ? exp((double)z - (double)m) : 0.0;
+            wm.d[e] = y;
+            part += y;
+        }
+        den = warp_sum(part);
+    }
+#pragma unroll 2
+    for (int e = lane; e < E; e += 32) {
+        const float z = row[e], b = a.bias ? a.bias[e] : 0.0f;
+        const double v = SOFTMAX ? wm.d[e] / den + (double)b : sigmoid64(z, b);
+        wm.d[e] = z > neg_inf() && v == v ? v : neg_inf64();
+    }
+    __syncwarp();
+    unsigned kept = a.leaders;
+    const int LG = a.group_lanes;
+    if (a.o.top_groups < a.o.groups) {
+        const int my = lane / LG, last = my < a.o.groups ? (my + 1) * a.per : 0;
+        double x1 = neg_inf64(), x2 = neg_inf64();
+        for (int i = my * a.per + (lane & (LG - 1)); i < last; i += LG) {
+            const double x = wm.d[i];
+            x2 = fmax(x2, fmin(x1, x));
+            x1 = fmax(x1, x);
+        }
+        for (int o = 1; o < LG; o <<= 1) {
+            const double y1 = __shfl_xor_sync(kFull, x1, o), y2 = __shfl_xor_sync(kFull, x2, o);
+            x2 = fmax(fmin(x1, y1), fmax(x2, y2));
+            x1 = fmax(x1, y1);
+        }
+        const double gv = a.o.group_top == 2 && x2 != neg_inf64() ? x1 + x2 : x1;
+        int ahead = 0;
+        for (int g = 0; g < a.o.groups; ++g) {
+            const double x = __shfl_sync(kFull, gv, g * LG);
+            ahead += x > gv || (x == gv && g < my);
+        }
+        kept = __ballot_sync(kFull, gv != neg_inf64() && ahead < a.o.top_groups) & a.leaders;
+    }
+    // the values as integers of the same order, 0 where there is none
+    unsigned long long key[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int e = lane + 32 * j;
+        key[j] = 0;
+        if (e < E && (kept >> ((e * a.per_inv >> 16) * LG & 31) & 1u)) {
+            const long long v = __double_as_longlong(wm.d[e] + 0.0);  // -0 -> 0
+            if (v != (long long)0xfff0000000000000ll) key[j] = (unsigned long long)(v ^ (v >> 63 | (1ll << 63)));
+        }
+    }
+    int mine = -1;
+#pragma unroll 1
+    for (int r = 0; r < k; ++r) {
+        unsigned long long x = key[0];
+        int e = lane;
+#pragma unroll
+        for (int j = 1; j < N; ++j)
+            if (key[j] > x) {
+                x = key[j];
+                e = lane + 32 * j;
+            }
+        const unsigned hi = __reduce_max_sync(kFull, (unsigned)(x >> 32));
+        bool own = (unsigned)(x >> 32) == hi;
+        const unsigned lo = __reduce_max_sync(kFull, own ? (unsigned)x : 0u);
+        if ((hi | lo) == 0u) break;
+        own &= (unsigned)x == lo;
+        e = (int)__reduce_min_sync(kFull, own ? (unsigned)e : ~0u);  // equal values: the lower expert
+        if (lane == r) mine = e;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (e == lane + 32 * j) key[j] = 0;
+    }
+    const bool live = mine >= 0;
+    const float z = live ? row[mine] : 0.0f;
+    float wt;
+    if (a.o.renormalize)
+        wt = k <= 8 ? chosen_share<8>(z, live, SOFTMAX) : chosen_share<16>(z, live, SOFTMAX);
+    else
+        wt = !live ? 0.0f : SOFTMAX ? (z == m ? 1.0f : expf(z - m)) * (float)(1.0 / den) : __fdividef(1.0f, 1.0f + expf(-z));
+    if (lane < k) {
+        a.idx[(size_t)t * k + lane] = mine;
+        a.w[(size_t)t * k + lane] = wt * a.o.scale;
+        if (live)
+            atomicAdd(&hist[mine], 1);
+        else
+            bad = true;
+    }
+    if (bad) report(a.status, kStDeviceCheck);
+    __syncwarp();
+}
+
+__device__ __forceinline__ float max8(float v) {  // over the 8 lanes of a token
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T sum8(T v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+constexpr int kQuadWarps = 8, kQuadTops = 81;  // float2 per token: 64 chunks, one gap per run, on shifting banks
+static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
+
+// Eight lanes per token, four tokens per warp: what a warp per token spends on
+// reductions, on the rounds of the choice and on the weights serves four.
+// Experts come in chunks of four; lane r of a token holds chunks r, r + 8, ..
+// (a 128-byte line per token and load).  A chunk never straddles two groups: a
+// run whose length is no multiple of four ends with a padded chunk.  Chunks
+// are sorted, their two best give the group values (through shared memory), and
+// the chunks of the kept groups are merged to the lane's four best.
+//
+// SCORED: the values compared are s + bias.  Otherwise (no bias, groups by
+// their best expert) they are the logits, whose order is that of the scores:
+// logits that differ by 2^-30 or more, and neither saturate (z <= 24, sigmoid)
+// nor underflow (600 below 0 or the largest), differ as 64-bit scores.
+//
+// Values too close are compared again by exact logits, or as 64-bit sigmoids, one
+// per lane.  What is left (closer still, NaN, +inf, too few experts, softmax
+// with a bias or sums of two) is done by route_token64.
+template <int NCH, bool SOFTMAX, bool SCORED>
+__global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
+    route_logits_quad_kernel(const __grid_constant__ RouteArgs a) {
+    constexpr int N = 4 * NCH;
+    constexpr uint32_t kTag = N - 1;
+    // the rounding of v and its low bits, (1 + 2 (N - 1)) 2^-24 < N 2^-23
+    constexpr float kTagErr = N * 0x1p-23f, kLogitErr = 0x1p-30f;
+    constexpr float kSaturated = 20.0f, kUnderflow = -600.0f;
+    extern __shared__ __align__(16) uint8_t smem[];
+    WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
+    float4* bias = reinterpret_cast<float4*>(smem + kQuadWarps * sizeof(WarpMem));  // by chunk; masked: kMasked
+    int* hist = reinterpret_cast<int*>(bias + 8 * NCH);
+    const int tid = threadIdx.x, lane = tid & 31, r = lane & 7, first_lane = lane & 24;
+    const int E = a.E, k = a.k, chunks = a.chunks;
+    if (SCORED)
+        for (int i = tid; i < 8 * N; i += kQuadWarps * 32) {
+            const int c = i >> 2, g = c * a.chunk_inv >> 16, off = 4 * (c - g * a.run_chunks) + (i & 3);
+            float b = kMasked;
+            if (c < chunks && off < a.run) {
+                b = a.bias ? a.bias[g * a.run + off] : 0.0f;
+                if (b != b) report(a.status, kStDeviceCheck);
+                b = b > neg_inf() ? fmaxf(fminf(b, kFltMax), -1e37f) : kMasked;
+            }
+            reinterpret_cast<float*>(bias)[i] = b;
+        }
+    for (int e = tid; e < E; e += kQuadWarps * 32) hist[e] = 0;
+    __syncthreads();
+
+    const bool vec = (a.run & 3) == 0, grouped = a.o.top_groups < a.o.groups;
+    uint32_t group_of = 0u;  // 4 bits per chunk
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) group_of |= (uint32_t)((r + 8 * i) * a.chunk_inv >> 16 & 15) << (4 * i);
+    const float rel_err = !SCORED || a.bias ? kTagErr : kRelErr;
+    float2* tops = reinterpret_cast<float2*>(wm.d) + (lane >> 3) * kQuadTops;
+    uint8_t* place = reinterpret_cast<uint8_t*>(wm.first) + (lane >> 3) * 16;  // lane of the s-th best
+    int* ranked = reinterpret_cast<int*>(wm.sorted) + (lane >> 3) * 9;         // expert of the s-th, compared again
+    static_assert(4 * 9 * sizeof(int) <= sizeof(wm.sorted) && 4 * 16 <= sizeof(wm.first), "");
+    // the expert of a value found in lane `from`
+    const auto expert = [&](float value, int from) {
+        const int j = (int)(__float_as_uint(value) & kTag), c = from + 8 * (j >> 2);
+        const int g = vec ? 0 : c * a.chunk_inv >> 16;
+        return g * a.run + 4 * (c - g * a.run_chunks) + (j & 3);
+    };
+    // exact logits whose scores' order they do not tell
+    const auto too_close = [](double x, double y) {
+        return !SCORED && x != y && fabs(x - y) < (!SOFTMAX && fmax(x, y) > 13.0 ? 0x1p-16 : (double)kLogitErr);
+    };
+
+    const int quads = (a.T - 1) / 4 + 1;
+    for (int q = (tid >> 5) * gridDim.x + blockIdx.x; q < quads; q += gridDim.x * kQuadWarps) {
+        const int t = 4 * q + (lane >> 3);
+        const bool in = t < a.T;  // else the last token once more, not stored
+        const float* row = a.logits + (size_t)(in ? t : a.T - 1) * E;
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = r + 8 * i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = kMasked;
+            if (8 * i < chunks) {
+                if (vec) {
+                    if (c < chunks) {
+                        const float4 x = *reinterpret_cast<const float4*>(row + 4 * c);
+                        v[4 * i] = x.x;
+                        v[4 * i + 1] = x.y;
+                        v[4 * i + 2] = x.z;
+                        v[4 * i + 3] = x.w;
+                    }
+                } else {
+                    const int g = group_of >> (4 * i) & 15, off = 4 * (c - g * a.run_chunks);
+                    const float* p = row + g * a.run + off;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c < chunks && off + j < a.run) v[4 * i + j] = p[j];
+                }
+            }
+        }
+        float nf = 0.0f;  // NaN where a logit is not finite
+#pragma unroll
+        for (int j = 0; j < N; ++j) nf = fmaf(v[j], 0.0f, nf);
+        const bool special = __any_sync(kFull, nf != nf);
+        unsigned masked = 0u;
+        bool again = false;
+        float m = 0.0f, top = 1.0f;  // softmax: the largest logit; a bound of the scores
+        if (special) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                again |= v[j] != v[j] || v[j] > kFltMax;
+                if (!(v[j] > neg_inf())) masked |= 1u << j;
+            }
+        }
+        if (SOFTMAX && (SCORED || !a.o.renormalize)) {
+            m = v[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j) m = fmaxf(m, v[j]);  // NaN drops out
+            m = max8(m);
+            again |= !(m > kLow);
+            float part = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float y = ex2_fast((v[j] - m) * kLog2e);
+                if (SCORED) v[j] = y;
+                part += y;
+            }
+            top = rcp_fast(fmaxf(sum8(part), 1e-30f));
+        }
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            if (8 * i >= chunks) continue;
+            float b[4] = {};
+            if (SCORED) *reinterpret_cast<float4*>(b) = bias[r + 8 * i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float& x = v[4 * i + j];
+                if (SCORED) x = SOFTMAX ? fmaf(x, top, b[j]) : rcp_fast(1.0f + ex2_fast(x * -kLog2e)) + b[j];
+                x = tagged<kTag>(x, 4 * i + j);
+                if (special && (masked >> (4 * i + j) & 1u)) x = kMasked;
+            }
+            order(v[4 * i], v[4 * i + 1]);
+            order(v[4 * i + 2], v[4 * i + 3]);
+            order(v[4 * i], v[4 * i + 2]);
+            order(v[4 * i + 1], v[4 * i + 3]);
+            order(v[4 * i + 1], v[4 * i + 2]);
+        }
+        const float abs_err = !SCORED ? kLogitErr : a.bias ? top * kAbsErr : 0.0f;
+
+        __syncwarp();  // the last tokens' readers are done
+        unsigned kept = 0xffu;
+        if (grouped) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+                if (r + 8 * i < chunks)
+                    tops[r + 8 * i + (group_of >> (4 * i) & 15)] = make_float2(v[4 * i], v[4 * i + 1]);
+            __syncwarp();
+            float x1 = kMasked, x2 = kMasked;
+            const bool real = r < a.o.groups;
+            const float2* mine = tops + (real ? r : 0) * (a.run_chunks + 1);
+            for (int i = 0; i < a.run_chunks; ++i) {
+                const float2 y = mine[i];
+                if (SCORED) x2 = fmaxf(fminf(x1, y.x), fmaxf(x2, y.y));
+                x1 = fmaxf(x1, y.x);
+            }
+            const bool two = SCORED && a.o.group_top == 2 && x2 > kLow;
+            float gv = two ? x1 + x2 : x1;
+            if (!real) gv = kMasked;
+            int ahead = 0;
+#pragma unroll
+            for (int o = 1; o < 8; ++o) ahead += __shfl_sync(kFull, gv, first_lane | ((r + o) & 7)) > gv;
+            bool keep = ahead < a.o.top_groups && gv > kLow;
+            kept = __ballot_sync(kFull, keep) >> first_lane & 0xffu;
+            // the last kept group against the best of the others
+            const float lo = -max8(keep ? -gv : kMasked), hi = max8(keep ? kMasked : gv);
+            const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
+            const bool unsure = __popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err));
+            if (!SCORED) again |= hi > kLow && (SOFTMAX ? lo < max8(gv) + kUnderflow : lo < kUnderflow || hi > kSaturated);
+            if (SCORED && SOFTMAX) {
+                again |= unsure;
+            } else if (__any_sync(kFull, unsure)) {
+                // the experts of the group's value, if no third (second) is close to them
+                const float cut = cut_of(two ? x2 : x1, abs_err, rel_err);
+                const bool any = real && x1 > kLow;
+                int found = 0, e1 = 0, e2 = 0;
+                for (int i = 0; i < a.run_chunks; ++i) {
+                    const float2 y = mine[i];
+                    const int e0 = r * a.run + 4 * i;
+                    if (any && y.x >= cut) {
+                        e2 = e1;
+                        e1 = e0 + (int)(__float_as_uint(y.x) & 3u);
+                        ++found;
+                    }
+                    if (any && y.y >= cut) {
+                        e2 = e1;
+                        e1 = e0 + (int)(__float_as_uint(y.y) & 3u);
+                        ++found;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
+                    if (r + 8 * i < chunks) tops[r + 8 * i + (group_of >> (4 * i) & 15)].x = v[4 * i + 2];
+                __syncwarp();
+                for (int i = 0; i < a.run_chunks; ++i) found += any && mine[i].x >= cut;
+                double x = neg_inf64();
+                if (any && SCORED) {
+                    x = sigmoid64(row[e1], a.bias ? a.bias[e1] : 0.0f);
+                    if (two) x += sigmoid64(row[e2], a.bias ? a.bias[e2] : 0.0f);
+                } else if (any) {
+                    x = row[e1];
+                }
+                bool unfit = any && found != (two ? 2 : 1);
+                int before = 0;
+#pragma unroll 1
+                for (int o = 1; o < 8; ++o) {
+                    const int g = (r + o) & 7;
+                    const double y = __shfl_sync(kFull, x, first_lane | g);
+                    before += y > x || (y == x && g < r);
+                    unfit |= too_close(x, y);
+                }
+                again |= unsure && unfit;
+                keep = unsure ? any && before < a.o.top_groups : keep;
+                kept = __ballot_sync(kFull, keep) >> first_lane & 0xffu;
+            }
+        }
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            if (i > 0 && 8 * i >= chunks) continue;
+            const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : kMasked;
+            if (i == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = v[j] + out;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = fmaxf(x[j], v[4 * i + 3 - j] + out);
+                order(x[0], x[2]);
+                order(x[1], x[3]);
+                order(x[0], x[1]);
+                order(x[2], x[3]);
+            }
+        }
+
+        // the k + 1 best in descending order, the s-th in lane s
+        float best = kMasked, mine = kMasked;
+        int taken = 0;
+#pragma unroll 1
+        for (int s = 0; s <= k; ++s) {
+            best = max8(x[0]);
+            const bool own = x[0] == best && best > kLow;
+            if (own) place[s] = (uint8_t)r;
+            if (r == s) mine = best;
+            x[0] = own ? x[1] : x[0];
+            x[1] = own ? x[2] : x[1];
+            x[2] = own ? x[3] : x[2];
+            x[3] = own ? kMasked : x[3];
+            taken += own;
+            if (__any_sync(kFull, own && taken >= 4 && s < k)) {  // a lane without any left takes its next best
+                float y = kMasked;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    if (8 * i >= chunks) continue;
+                    const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : kMasked;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float u = v[4 * i + j] + out;
+                        if (u < best) y = fmaxf(y, u);
+                    }
+                }
+                if (own && taken >= 4) x[0] = y;
+            }
+        }
+        // every round one lane's (the last may find no expert left)
+        again |= sum8(taken) != k + (best > kLow);
+        float next = __shfl_down_sync(kFull, mine, 1);
+        if (r == k - 1) next = best;
+        if (!SCORED) {
+            const float least = SOFTMAX ? __shfl_sync(kFull, mine, first_lane) + kUnderflow : kUnderflow;
+            again |= r < k && (mine < least || (!SOFTMAX && mine > kSaturated));
+        }
+        const bool close = r < k && !(mine - next > abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f);
+        if (SCORED && SOFTMAX) again |= close;
+        unsigned redo = __ballot_sync(kFull, again && in);
+        __syncwarp();
+        bool live = r < k && in && (redo >> first_lane & 0xffu) == 0u;
+        int e = live ? expert(mine, place[r]) : 0;
+        if (!(SCORED && SOFTMAX) && __any_sync(kFull, close && live)) {
+            // the k, and the next where it is close to the last, by what their order is defined on
+            const bool sure = !__any_sync(kFull, close && live && r == k - 1);
+            bool border = false, unfit = false;
+            int en = 0;
+            if (!sure) {
+                border = (__ballot_sync(kFull, close && live && r == k - 1) >> first_lane & 0xffu) != 0u;
+                const float cut = cut_of(best, abs_err, rel_err);
+                int all = 0;  // values that may be among the k
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    if (8 * i >= chunks) continue;
+                    const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : kMasked;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) all += v[4 * i + j] + out >= cut;
+                }
+                unfit = sum8(all) != k + 1 && border;
+                border &= !unfit;
+                if (border) en = expert(best, place[k]);
+            }
+            double u = row[e], n = row[en];
+            if (SCORED) {
+                u = sigmoid64((float)u, a.bias ? a.bias[e] : 0.0f);
+                if (!sure) n = sigmoid64((float)n, a.bias ? a.bias[en] : 0.0f);
+            }
+            int rank = 0;
+#pragma unroll 1
+            for (int s = 0; s < k; ++s) {
+                const double y = __shfl_sync(kFull, u, first_lane | s);
+                const int f = __shfl_sync(kFull, e, first_lane | s);
+                rank += y > u || (y == u && f < e);
+                unfit |= r < k && too_close(u, y);
+            }
+            const bool behind = border && r < k && (n > u || (n == u && en < e));  // the next one overtakes it
+            unfit |= border && r < k && too_close(u, n);
+            rank += behind;
+            const int overtaken = __popc(__ballot_sync(kFull, behind) >> first_lane & 0xffu);
+            if (r < k && rank < k) ranked[rank] = e;
+            if (r == 0 && overtaken > 0) ranked[k - overtaken] = en;
+            __syncwarp();
+            if (live) e = ranked[r];
+            redo |= __ballot_sync(kFull, unfit && in);
+            live &= (redo >> first_lane & 0xffu) == 0u;
+            if (!live) e = 0;
+            __syncwarp();
+        }
+        const float z = live ? row[e] : 0.0f;
+        float wt;
+        if (a.o.renormalize)
+            wt = chosen_share<8>(z, live, SOFTMAX);
+        else
+            wt = !live ? 0.0f : SOFTMAX ? (z == m ? top : expf(z - m) * top) : __fdividef(1.0f, 1.0f + expf(-z));
+        if (live) {
+            a.idx[(size_t)t * k + r] = e;
+            a.w[(size_t)t * k + r] = wt * a.o.scale;
+            atomicAdd(&hist[e], 1);
+        }
+        for (unsigned rest = redo; rest;) {  // warp-uniform
+            const int which = (__ffs(rest) - 1) >> 3;
+            rest &= ~(0xffu << (8 * which));
+            route_token64<SOFTMAX>(a, wm, hist, 4 * q + which, lane);
+        }
+    }
+    __syncthreads();
+    grid_dependency_wait();  // the counters are clear
+    for (int e = tid; e < E; e += kQuadWarps * 32)
+        if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
 }
 
 // Clears the counters.  The routing kernel starts beside it, once everything
@@ -862,6 +1365,28 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
     return a.o.softmax ? launch_route<VPT, true, 8, false>(a, grid, st) : launch_route<VPT, false, 8, false>(a, grid, st);
 }
 
+template <int NCH, bool SOFTMAX, bool SCORED>
+cudaError_t launch_quad_s(const RouteArgs& a, int num_sms, cudaStream_t st) {
+    auto kern = route_logits_quad_kernel<NCH, SOFTMAX, SCORED>;
+    constexpr size_t smem = kQuadWarps * sizeof(WarpMem) + 8 * NCH * sizeof(float4) + kMaxExperts * sizeof(int);
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    note_launches(2);
+    err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);
+    if (err != cudaSuccess) return err;
+    const int blocks = (a.T - 1) / (4 * kQuadWarps) + 1, most = (NCH == 8 ? 3 : 4) * num_sms;
+    return launch_after(kern, dim3((unsigned)(blocks < most ? blocks : most)), kQuadWarps * 32, smem, 1, st, a);
+}
+
+template <int NCH>
+cudaError_t launch_quad(const RouteArgs& a, int num_sms, cudaStream_t st) {
+    if (a.bias || (a.o.top_groups < a.o.groups && a.o.group_top == 2))
+        return a.o.softmax ? launch_quad_s<NCH, true, true>(a, num_sms, st)
+                           : launch_quad_s<NCH, false, true>(a, num_sms, st);
+    return a.o.softmax ? launch_quad_s<NCH, true, false>(a, num_sms, st)
+                       : launch_quad_s<NCH, false, false>(a, num_sms, st);
+}
+
 template <int VPT>
 cudaError_t launch_bwd_v(const RouteBwdArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T - 1) / kBwdWarps + 1);
@@ -882,7 +1407,11 @@ cudaError_t launch_bwd_chosen(const RouteBwdArgs& a, cudaStream_t st) {
 cudaError_t launch_route_logits(const float* logits, const float* bias, int T, int E, int k, const RouteOpts& o,
                                 int32_t* idx, float* w, int32_t* counts, int* status, int num_sms, cudaStream_t st) {
     if (T == 0) return cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)E, st);
-    const int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
+    const bool grouped = o.top_groups < o.groups;
+    const int run = grouped ? E / o.groups : E, run_chunks = (run + 3) / 4, chunks = run_chunks * (E / run);
+    const bool quad = T > kQuadTokens && k <= 8 && (!grouped || o.groups <= 8) && chunks <= 64;
+    int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
+    if (quad) vpt = chunks <= 16 ? 2 : chunks <= 32 ? 4 : 8;  // chunks per lane; then E <= 32 vpt as well
     const int per = E / o.groups, whole = per % vpt == 0 ? per / vpt : 0;
     int lanes = whole > 0 && (whole & (whole - 1)) == 0 ? whole : 1;
     if (whole != lanes)
@@ -893,7 +1422,12 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
     // best k + 1 then ask a lane of 8 experts for a fifth in 0.2% of the tokens.
     const bool direct = lanes * vpt == per && (vpt <= 4 || o.top_groups * lanes >= 16);
     const RouteArgs a{logits, bias,   T,      E, k, per, (65536 + per - 1) / per, lanes,
-                      direct, leaders, o, idx, w, counts, status};
+                      direct, leaders, run, run_chunks, chunks, (65536 + run_chunks - 1) / run_chunks, o, idx, w, counts,
+                      status};
+    if (quad)
+        return vpt == 2   ? launch_quad<2>(a, num_sms, st)
+               : vpt == 4 ? launch_quad<4>(a, num_sms, st)
+                          : launch_quad<8>(a, num_sms, st);
     switch (vpt) {
         case 1: return launch_route_v<1>(a, num_sms, st);
         case 2: return launch_route_v<2>(a, num_sms, st);
