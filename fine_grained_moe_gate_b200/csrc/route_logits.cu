@@ -29,7 +29,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxK = 16;
-constexpr int kQuadTokens = 128;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ double neg_inf64() { return __longlong_as_double(0xfff0000000000000ll); }
@@ -785,7 +784,8 @@ __device__ __forceinline__ T sum8(T v) {
     return v;
 }
 
-constexpr int kQuadWarps = 8, kQuadTops = 81;  // float2 per token: 64 chunks, one gap per run, on shifting banks
+constexpr int kQuadWarps = 16, kQuadCtas = 2;  // CTAs per SM
+constexpr int kQuadTops = 81;  // float2 per token: 64 chunks, one gap per run, on shifting banks
 static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 
 // Eight lanes per token, four tokens per warp: what a warp per token spends on
@@ -796,17 +796,24 @@ static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 // are sorted, their two best give the group values (through shared memory), and
 // the chunks of the kept groups are merged to the lane's four best.
 //
-// SCORED: the values compared are s + bias.  Otherwise (no bias, groups by
+// SCORED: the values compared are sigmoid + bias.  Otherwise (no bias, groups by
 // their best expert) they are the logits, whose order is that of the scores:
 // logits that differ by 2^-30 or more, and neither saturate (z <= 24, sigmoid)
 // nor underflow (600 below 0 or the largest), differ as 64-bit scores.
 //
 // Values too close are compared again by exact logits, or as 64-bit sigmoids, one
-// per lane.  What is left (closer still, NaN, +inf, too few experts, softmax
-// with a bias or sums of two) is done by route_token64.
+// per lane (0.6% of the tokens of 256 normal logits with biases).  What is left
+// (closer still, NaN, +inf, too few experts) is done by route_token64, 6 us.
+//
+// Issue bound: 32768 x 256 sigmoid tokens with groups execute 466 instructions
+// each and take 22.4 us (a warp per token 34.6), 32768 x 160 softmax tokens 17.3
+// (36.1); 8192 x 256 10.2 (14.4).  16 warps per CTA, two CTAs per SM with 64
+// registers: three CTAs of 8 warps with 80 took 24.9, 20.0 and 9.9 us, one of 32
+// 22.3, 16.6 and 10.3.  Every CTA adds its counts with E atomics, so few are best.
 template <int NCH, bool SOFTMAX, bool SCORED>
-__global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
+__global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
     route_logits_quad_kernel(const __grid_constant__ RouteArgs a) {
+    static_assert(!(SOFTMAX && SCORED), "closer values would need the 64-bit sum");
     constexpr int N = 4 * NCH;
     constexpr uint32_t kTag = N - 1;
     // the rounding of v and its low bits, (1 + 2 (N - 1)) 2^-24 < N 2^-23
@@ -883,11 +890,12 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
         }
         float nf = 0.0f;  // NaN where a logit is not finite
 #pragma unroll
-        for (int j = 0; j < N; ++j) nf = fmaf(v[j], 0.0f, nf);
+        for (int j = 0; j < N; ++j)
+            if (8 * (j / 4) < chunks) nf = fmaf(v[j], 0.0f, nf);
         const bool special = __any_sync(kFull, nf != nf);
         unsigned masked = 0u;
         bool again = false;
-        float m = 0.0f, top = 1.0f;  // softmax: the largest logit; a bound of the scores
+        float m = 0.0f, top = 1.0f;  // softmax as scored: the largest logit and its score
         if (special) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -895,18 +903,18 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
                 if (!(v[j] > neg_inf())) masked |= 1u << j;
             }
         }
-        if (SOFTMAX && (SCORED || !a.o.renormalize)) {
+        if (SOFTMAX && !a.o.renormalize) {
             m = v[0];
 #pragma unroll
-            for (int j = 1; j < N; ++j) m = fmaxf(m, v[j]);  // NaN drops out
+            for (int j = 1; j < N; ++j)
+                if (8 * (j / 4) < chunks) m = fmaxf(m, v[j]);  // NaN drops out
             m = max8(m);
             again |= !(m > kLow);
             float part = 0.0f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float y = ex2_fast((v[j] - m) * kLog2e);
-                if (SCORED) v[j] = y;
-                part += y;
+                if (8 * (j / 4) >= chunks) continue;
+                part += ex2_fast((v[j] - m) * kLog2e);
             }
             top = rcp_fast(fmaxf(sum8(part), 1e-30f));
         }
@@ -918,17 +926,25 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float& x = v[4 * i + j];
-                if (SCORED) x = SOFTMAX ? fmaf(x, top, b[j]) : rcp_fast(1.0f + ex2_fast(x * -kLog2e)) + b[j];
+                if (SCORED) x = rcp_fast(1.0f + ex2_fast(x * -kLog2e)) + b[j];
                 x = tagged<kTag>(x, 4 * i + j);
-                if (special && (masked >> (4 * i + j) & 1u)) x = kMasked;
             }
+        }
+        if (special) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (masked >> j & 1u) v[j] = kMasked;
+        }
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            if (8 * i >= chunks) continue;
             order(v[4 * i], v[4 * i + 1]);
             order(v[4 * i + 2], v[4 * i + 3]);
             order(v[4 * i], v[4 * i + 2]);
             order(v[4 * i + 1], v[4 * i + 3]);
             order(v[4 * i + 1], v[4 * i + 2]);
         }
-        const float abs_err = !SCORED ? kLogitErr : a.bias ? top * kAbsErr : 0.0f;
+        const float abs_err = !SCORED ? kLogitErr : a.bias ? kAbsErr : 0.0f;
 
         __syncwarp();  // the last tokens' readers are done
         unsigned kept = 0xffu;
@@ -958,10 +974,9 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
             const float lo = -max8(keep ? -gv : kMasked), hi = max8(keep ? kMasked : gv);
             const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
             const bool unsure = __popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err));
-            if (!SCORED) again |= hi > kLow && (SOFTMAX ? lo < max8(gv) + kUnderflow : lo < kUnderflow || hi > kSaturated);
-            if (SCORED && SOFTMAX) {
-                again |= unsure;
-            } else if (__any_sync(kFull, unsure)) {
+            const float least = SOFTMAX && !SCORED ? max8(gv) + kUnderflow : kUnderflow;  // a shuffle: by every lane
+            if (!SCORED) again |= hi > kLow && (lo < least || (!SOFTMAX && hi > kSaturated));
+            if (__any_sync(kFull, unsure)) {
                 // the experts of the group's value, if no third (second) is close to them
                 const float cut = cut_of(two ? x2 : x1, abs_err, rel_err);
                 const bool any = real && x1 > kLow;
@@ -1011,7 +1026,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             if (i > 0 && 8 * i >= chunks) continue;
-            const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : kMasked;
+            const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : neg_inf();
             if (i == 0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = v[j] + out;
@@ -1044,7 +1059,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
                     if (8 * i >= chunks) continue;
-                    const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : kMasked;
+                    const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : neg_inf();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float u = v[4 * i + j] + out;
@@ -1054,6 +1069,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
                 if (own && taken >= 4) x[0] = y;
             }
         }
+        best = fmaxf(best, kMasked);
         // every round one lane's (the last may find no expert left)
         again |= sum8(taken) != k + (best > kLow);
         float next = __shfl_down_sync(kFull, mine, 1);
@@ -1063,12 +1079,11 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
             again |= r < k && (mine < least || (!SOFTMAX && mine > kSaturated));
         }
         const bool close = r < k && !(mine - next > abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f);
-        if (SCORED && SOFTMAX) again |= close;
         unsigned redo = __ballot_sync(kFull, again && in);
         __syncwarp();
         bool live = r < k && in && (redo >> first_lane & 0xffu) == 0u;
         int e = live ? expert(mine, place[r]) : 0;
-        if (!(SCORED && SOFTMAX) && __any_sync(kFull, close && live)) {
+        if (__any_sync(kFull, close && live)) {
             // the k, and the next where it is close to the last, by what their order is defined on
             const bool sure = !__any_sync(kFull, close && live && r == k - 1);
             bool border = false, unfit = false;
@@ -1080,7 +1095,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, NCH == 8 ? 3 : 4)
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
                     if (8 * i >= chunks) continue;
-                    const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : kMasked;
+                    const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : neg_inf();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) all += v[4 * i + j] + out >= cut;
                 }
@@ -1374,15 +1389,15 @@ cudaError_t launch_quad_s(const RouteArgs& a, int num_sms, cudaStream_t st) {
     note_launches(2);
     err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);
     if (err != cudaSuccess) return err;
-    const int blocks = (a.T - 1) / (4 * kQuadWarps) + 1, most = (NCH == 8 ? 3 : 4) * num_sms;
-    return launch_after(kern, dim3((unsigned)(blocks < most ? blocks : most)), kQuadWarps * 32, smem, 1, st, a);
+    // over all SMs first, then more warps of each: rounds of one quad per warp of an SM's CTA
+    const int quads = (a.T - 1) / 4 + 1, rounds = (quads - 1) / (kQuadWarps * num_sms) + 1;
+    const int grid = quads < num_sms ? quads : (rounds < kQuadCtas ? rounds : kQuadCtas) * num_sms;
+    return launch_after(kern, dim3((unsigned)grid), kQuadWarps * 32, smem, 1, st, a);
 }
 
 template <int NCH>
-cudaError_t launch_quad(const RouteArgs& a, int num_sms, cudaStream_t st) {
-    if (a.bias || (a.o.top_groups < a.o.groups && a.o.group_top == 2))
-        return a.o.softmax ? launch_quad_s<NCH, true, true>(a, num_sms, st)
-                           : launch_quad_s<NCH, false, true>(a, num_sms, st);
+cudaError_t launch_quad(const RouteArgs& a, bool scored, int num_sms, cudaStream_t st) {
+    if (scored) return launch_quad_s<NCH, false, true>(a, num_sms, st);
     return a.o.softmax ? launch_quad_s<NCH, true, false>(a, num_sms, st)
                        : launch_quad_s<NCH, false, false>(a, num_sms, st);
 }
@@ -1409,7 +1424,15 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
     if (T == 0) return cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)E, st);
     const bool grouped = o.top_groups < o.groups;
     const int run = grouped ? E / o.groups : E, run_chunks = (run + 3) / 4, chunks = run_chunks * (E / run);
-    const bool quad = T > kQuadTokens && k <= 8 && (!grouped || o.groups <= 8) && chunks <= 64;
+    // Four tokens per warp, where there are enough of them: a quad takes longer
+    // than a token (us for 1024, 2048, 4096 tokens, a warp per token against four:
+    // 256 experts sigmoid with bias 5.5 6.1 9.1, 7.8 7.8 8.0, 128 experts 5.0 6.3 7.4,
+    // 5.5 5.6 5.8; without bias, 256 experts softmax 6.6 7.7 9.2, 6.1 6.4 6.7, 64
+    // experts 6.0 6.2 8.1, 3.9 4.1 4.3).  Softmax with a bias or sums of two stays
+    // with a warp per token: its close values need the sum in 64 bits.
+    const bool scored = bias || (grouped && o.group_top == 2);
+    const bool quad = T >= (scored ? 13 : 3) * E && T > 128 && !(scored && o.softmax) && k <= 8 &&
+                      (!grouped || o.groups <= 8) && chunks <= 64;
     int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
     if (quad) vpt = chunks <= 16 ? 2 : chunks <= 32 ? 4 : 8;  // chunks per lane; then E <= 32 vpt as well
     const int per = E / o.groups, whole = per % vpt == 0 ? per / vpt : 0;
@@ -1425,9 +1448,9 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
                       direct, leaders, run, run_chunks, chunks, (65536 + run_chunks - 1) / run_chunks, o, idx, w, counts,
                       status};
     if (quad)
-        return vpt == 2   ? launch_quad<2>(a, num_sms, st)
-               : vpt == 4 ? launch_quad<4>(a, num_sms, st)
-                          : launch_quad<8>(a, num_sms, st);
+        return vpt == 2   ? launch_quad<2>(a, scored, num_sms, st)
+               : vpt == 4 ? launch_quad<4>(a, scored, num_sms, st)
+                          : launch_quad<8>(a, scored, num_sms, st);
     switch (vpt) {
         case 1: return launch_route_v<1>(a, num_sms, st);
         case 2: return launch_route_v<2>(a, num_sms, st);

@@ -486,7 +486,8 @@ MOE_API moe_status moe_gate_logits(const void* x, const void* w_gate, moe_shape 
  * with fewer than k experts to choose from gets index -1 and weight 0 in the
  * slots left, and is reported likewise.  logit +inf: the limit of the formula.
  * logits [T][E] fp32; of sh only T, E and k matter here (the rest has to be
- * valid).  Results do not depend on T or on a token's place. */
+ * valid).  Indices, and weights except softmax ones as scored (last bits of
+ * their sum), do not depend on T or on a token's place. */
 MOE_API moe_status moe_route_logits(const float* logits, const float* bias, moe_shape sh, moe_route_opts opts,
                                     int32_t* topk_idx, float* topk_w, int32_t* counts, void* stream);
 

@@ -453,3 +453,140 @@ def test_streams_and_strided_inputs():
     wide = torch.empty((3000, 512), device=DEV)
     with pytest.raises(moe.MoEError, match="contiguous"):
         moe.moe_route_logits(wide[:, :256], bias, shape(3000, 256, 8), co, idx, w, counts)
+
+
+# ---------------------------------------------------------------- batches large enough for four tokens per warp
+
+BATCHES = [(131, 5, 2), (300, 16, 8), (901, 60, 4), (835, 63, 7), (1031, 64, 6), (1709, 130, 8), (2083, 160, 6), (3350, 251, 8),
+           (3331, 256, 1), (3400, 256, 8), (3329, 256, 9)]
+
+
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("name", ["sigmoid", "softmax_as_scored", "softmax"])
+@pytest.mark.parametrize("T,E,k", BATCHES)
+def test_batch_matches_oracle(T, E, k, name, with_bias):
+    z, bias = make(T, E, T + E, 1.5)
+    assert not check_route(z, bias if with_bias else None, k, OPTS[name]).any()
+    check_status()
+
+
+@pytest.mark.parametrize("groups,per,top,k", [(8, 32, 4, 8), (8, 20, 3, 6), (6, 42, 3, 8), (6, 9, 2, 7), (8, 31, 4, 8), (3, 5, 2, 8),
+                                              (2, 128, 1, 8), (4, 63, 2, 8), (8, 2, 4, 8), (7, 36, 5, 8), (8, 1, 8, 8),
+                                              (8, 1, 3, 3), (5, 4, 2, 8), (4, 16, 1, 8)])
+@pytest.mark.parametrize("score,gtop", [("sigmoid", 1), ("sigmoid", 2), ("softmax", 1)])
+def test_batch_group_shapes(groups, per, top, k, score, gtop):
+    E = groups * per
+    z, bias = make(max(13 * E, 129) + 2, E, groups * 100 + per, 2.0)
+    o = ot.Opts(score=score, groups=groups, top_groups=top, group_top=gtop, scale=2.5)
+    check_route(z, bias if score == "sigmoid" else None, k, o)
+    check_route(z, None, k, o)
+    check_status()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("gtop", [0, 1, 2])
+def test_batch_ties_go_to_the_lower_index(score, gtop):
+    g = torch.Generator(device=DEV).manual_seed(15)
+    z = torch.randint(-2, 3, (3333, 256), generator=g, device=DEV).float() * 0.5
+    o = ot.Opts(score=score, groups=8, top_groups=3, group_top=gtop) if gtop else ot.Opts(score=score)
+    check_route(z, None, 8, o)
+    check_route(z, torch.full((256,), 0.25, device=DEV), 8, o)
+    z[:, ::3] += torch.randint(-99, 99, (3333, 86), generator=g, device=DEV).float() / 64  # some ties, most rows without
+    check_route(z, None, 7, o)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_batch_values_closer_than_their_32_bit_error(score):
+    T, E = 1250, 96
+    rng = np.random.default_rng(16)
+    z = torch.from_numpy(rng.normal(size=(T, E)).astype(np.float32)).to(DEV)
+    z[:, 1::2] = torch.nextafter(z[:, ::2], torch.from_numpy(np.where(rng.random((T, E // 2)) < 0.5, -9.0, 9.0)
+                                                               .astype(np.float32)).to(DEV))
+    for o in (ot.Opts(score=score), ot.Opts(score=score, groups=6, top_groups=3, group_top=2),
+              ot.Opts(score=score, groups=6, top_groups=3, group_top=1)):
+        for k in (7, 8):
+            check_route(z, None, k, o)
+            check_route(z, torch.full((E,), 0.03125, device=DEV), k, o)
+    # groups whose values differ by an ulp of one logit
+    z[:, 16:32], z[:, 48:64] = z[:, :16], z[:, 32:48]
+    z[:, 16::32] = torch.nextafter(z[:, ::32], torch.tensor(9.0, device=DEV))
+    for gtop in (1, 2):
+        check_route(z, None, 8, ot.Opts(score=score, groups=6, top_groups=3, group_top=gtop))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("kind", ["saturated", "beyond", "tiny", "wide", "huge"])
+def test_batch_logits_whose_scores_lie_close(score, kind):
+    T, E = 515, 32
+    g = torch.Generator(device=DEV).manual_seed(17)
+    u = torch.rand((T, E), generator=g, device=DEV)
+    z = {"saturated": 12 + 10 * u, "beyond": 25 + 25 * u, "tiny": (u - 0.5) * 1e-12, "wide": (u - 0.5) * 3000,
+         "huge": (u - 0.5) * 6e38}[kind]
+    if kind == "huge" and score == "softmax":
+        z = z.clamp(min=-1e37)  # rows of +inf (6e38 is past the type) beside one low value
+    for o in (ot.Opts(score=score), ot.Opts(score=score, groups=4, top_groups=2, group_top=1)):
+        idx, w, counts = run_route(z, None, 6, o)
+        zn = z.cpu().numpy()
+        ri, rw, rc, _ = ot.route(zn, None, 6, o)
+        if kind == "tiny":
+            # Logits closer than 2^-52: their order is that of two libraries' exp, each within an ulp.  Around
+            # s = 1/2 (e^-z = 1, ulp 2^-52): e off by 2^-52, 1 + e rounded by 2^-53, s = 1 / (1 + e) off by a quarter
+            # of their sum and 2^-54: D = 1.5 x 2^-53.  Softmax, s = y / sum = 1/32: y off by its ulp 2^-53, the quotient
+            # rounded by 2^-53 of it: D = 2^-57.  The r-th largest of values off by at most
+            # D is within D of the r-th largest, so the oracle's scores of both choices differ by at most 4 D, 6 x 2^-53
+            # and 2^-55 (2^-54 with the sums' own rounding).  Groups as close as that may be exchanged.
+            s, near = ot.scores(zn, score), 6 * 2.0 ** -53 if score == "sigmoid" else 2.0 ** -54
+            sure = np.ones(T, bool)
+            if o.groups > 1:
+                gv = np.sort(s.reshape(T, o.groups, -1).max(axis=2), axis=1)[:, ::-1]
+                sure = gv[:, o.top_groups - 1] - gv[:, o.top_groups] > near
+            at = lambda i: np.take_along_axis(s, i, axis=1)
+            assert (np.abs(at(idx) - at(ri)) <= near)[sure].all() and sure.mean() > 0.9
+            assert (np.diff(np.sort(idx, axis=1), axis=1) > 0).all()
+            rw = np.stack([ot.chosen_weights(zn[t, i].astype(np.float64), s[t, i], o) for t, i in enumerate(idx)])
+            rc = np.bincount(idx.reshape(-1), minlength=E)
+        else:
+            assert (idx == ri).all(), np.argwhere(idx != ri)[:5]
+        assert (counts == rc).all()
+        # e^x for |x| up to 87 (what is smaller underflows): 2 x 87 u of the argument's rounding
+        assert (np.abs(w - rw) <= (32 + 2 * 87) * U * np.abs(rw) + TINY).all()
+
+
+@pytest.mark.parametrize("name", ["sigmoid", "softmax", "softmax_as_scored"])
+def test_batch_best_experts_in_one_lane(name):
+    """Experts 32 apart in chunks of four are one lane's: 4, 5 .. 20 of the best lie there."""
+    T, E, k = 3400, 256, 8
+    g = torch.Generator(device=DEV).manual_seed(18)
+    z, bias = make(T, E, 18)
+    lane = torch.randint(0, 8, (T, 1), generator=g, device=DEV)
+    many = 3 + torch.arange(T, device=DEV)[:, None] % 18
+    e = torch.arange(E, device=DEV)[None]
+    here = (e // 4 % 8 == lane) & ((e // 32) * 4 + e % 4 < many)
+    z = torch.where(here, z.abs() + 4.0, z)
+    check_route(z, None, k, OPTS[name])
+    check_route(z, bias, k, OPTS[name])
+    check_route(z, None, k, ot.Opts(score=OPTS[name].score, groups=8, top_groups=5, group_top=1))
+    check_status()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_batch_masks_infinities_and_nan(score):
+    T, E, k = 1003, 60, 6
+    z, bias = make(T, E, 19)
+    inf = float("inf")
+    z[:, 7] = -inf
+    z[0:40, : E - k] = -inf  # exactly k left
+    z[100:103, : E - k + 2] = -inf  # too few
+    z[200] = -inf  # none
+    z[300:303, 11] = inf
+    z[301, 12] = inf
+    z[400, 13] = float("nan")
+    z[401] = float("nan")
+    z[T - 1, 5:] = -inf
+    bias[3] = -inf
+    bias[4] = 2e38
+    for b in (None, bias):
+        for o in (ot.Opts(score=score), ot.Opts(score=score, groups=5, top_groups=2, group_top=1)):
+            moe.moe_get_last_error()
+            assert check_route(z, b, k, o).any()
+            assert moe.moe_get_last_error() == 6
