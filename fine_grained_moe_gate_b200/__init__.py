@@ -123,6 +123,9 @@ def saved_acts(t: dict) -> MoESavedActs:
             raise MoEError(1, f"saved_acts: {n} must be on one device with the others, got {v.device}")
         device, out.sizes[n] = v.get_device(), _nbytes(v)
     out.device = device  # -1: the CPU, which the calls refuse
+    # elements each expert set's buffers hold (a tile of 32 has a scale byte)
+    out.room = {pre: min([out.sizes[n] * (32 if n.endswith("scale") else 1) for n in (pre + "a", pre + "a_scale",
+                          pre + "g", pre + "g_scale") if n in out.sizes], default=None) for pre in ("", "s")}
     return out
 
 
@@ -214,11 +217,22 @@ def _p(t):
 def _stream(stream, device=None):
     if stream is None:
         import torch
-        if device is None:
-            device = torch.cuda.current_device()
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without a Stream object (3 us)
-        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+        return _handles()[1](torch.cuda.current_device() if device is None else device)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_bound: tuple = ()
+
+
+def _handles():
+    """The current device, and a device's current stream as a raw handle: torch's own short ways to them where it has
+    these (a Stream object costs 3 us)."""
+    global _bound
+    if not _bound:
+        import torch
+        _bound = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                  getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return _bound
 
 
 def _check(status: int, where: str):
@@ -231,6 +245,22 @@ def _nbytes(t) -> int:
 
 
 _dtypes: dict = {}
+_functions: dict = {}
+
+
+def _prepare():
+    import torch
+    _dtypes.update((n, getattr(torch, n)) for n in ("float32", "bfloat16", "int32", "uint8"))
+    _functions.update((n, getattr(lib(), n)) for n in EXPORTS)
+
+
+def _refuse(name, what, t, dtype, n, dev):
+    if t.dtype is not _dtypes[dtype]:
+        raise MoEError(1, f"{name}: {what} must be {dtype}, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise MoEError(1, f"{name}: {what} must be contiguous with at least {n} elements, got {tuple(t.shape)}, strides "
+                          f"{t.stride()}")
+    raise MoEError(1, f"{name}: {what} must be on one CUDA device with the other tensors, got {t.device}")
 
 
 def _call(name, stream, *args):
@@ -240,31 +270,33 @@ def _call(name, stream, *args):
     the device of the others.  None and raw pointers go through as they are.
     The call runs with the tensors' device current, on its current stream
     unless one is given."""
-    import torch
     if not _dtypes:
-        _dtypes.update((n, getattr(torch, n)) for n in ("float32", "bfloat16", "int32", "uint8"))
+        _prepare()
     dev, out = -1, []
     for a in args:
         if type(a) is tuple:
             what, a, dtype, n = a
             if a is not None and type(a) is not int:
-                if a.dtype is not _dtypes[dtype]:
-                    raise MoEError(1, f"{name}: {what} must be {dtype}, got {a.dtype}")
-                if a.numel() < n or not a.is_contiguous():
-                    raise MoEError(1, f"{name}: {what} must be contiguous with at least {n} elements, got "
-                                      f"{tuple(a.shape)}, strides {a.stride()}")
                 d = a.get_device()
-                if d < 0 or 0 <= dev != d:
-                    raise MoEError(1, f"{name}: {what} must be on one CUDA device with the other tensors, got {a.device}")
+                if (d < 0 or dev != d and dev >= 0 or a.dtype is not _dtypes[dtype] or a.numel() < n
+                        or not a.is_contiguous()):
+                    _refuse(name, what, a, dtype, n, dev)
                 dev = d
                 a = a.data_ptr()
         out.append(a)
-    fn = getattr(lib(), name)
-    if dev < 0 or dev == torch.cuda.current_device():
-        _check(fn(*out, _stream(stream, dev if dev >= 0 else None)), name)
+    fn = _functions[name]
+    if dev < 0:
+        status = fn(*out, _stream(stream))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*out, _stream(stream, dev)), name)
+        device, raw_stream = _bound or _handles()
+        if dev == device():
+            status = fn(*out, raw_stream(dev) if stream is None else _stream(stream))
+        else:
+            import torch
+            with torch.cuda.device(dev):
+                status = fn(*out, _stream(stream, dev))
+    if status:
+        raise MoEError(status, name)
 
 
 def _saved_ref(name, saved, shape, sets, device=-1):
@@ -272,15 +304,14 @@ def _saved_ref(name, saved, shape, sets, device=-1):
     shared) hold the shape's rows, on the call's device."""
     if saved is None:
         return None
-    sizes = getattr(saved, "sizes", None)
-    if sizes:
+    room = getattr(saved, "room", None)
+    if room:
         for pre in sets:
-            rows, n = (shape.T * shape.k, shape.I) if pre == "" else (shape.T, shape.S * shape.Is)
-            for f, need in ((pre + "a", rows * n), (pre + "a_scale", rows * n // 32), (pre + "g", rows * n),
-                            (pre + "g_scale", rows * n // 32)):
-                if sizes.get(f, need) < need:
-                    raise MoEError(1, f"{name}: saved {f} needs {need} bytes, has {sizes[f]}")
-        if saved.device < 0 or 0 <= device != saved.device:
+            need = shape.T * shape.k * shape.I if pre == "" else shape.T * shape.S * shape.Is
+            if room[pre] is not None and room[pre] < need:
+                raise MoEError(1, f"{name}: the saved {pre}a, {pre}g and their scales need {need} and {need // 32} bytes, "
+                                  f"got {[saved.sizes.get(pre + n) for n in ('a', 'g', 'a_scale', 'g_scale')]}")
+        if saved.device is not None and (saved.device < 0 or 0 <= device != saved.device):
             raise MoEError(1, f"{name}: saved activations must be on the CUDA device of the other tensors")
     return ctypes.byref(saved)
 

@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(n_threads<PAIR>(), 1)
 template <int C, bool PAIR>
 cudaError_t launch_c(const CUtensorMap& tx, const CUtensorMap& tw, const GateParams& p, int tiles, int chunks,
                      size_t smem, cudaStream_t st) {
-    auto kern = gate_logits_kernel<C, PAIR>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_LIMIT);
+    constexpr auto kern = gate_logits_kernel<C, PAIR>;
+    const cudaError_t err = allow_smem<kern>(SMEM_LIMIT);
     if (err != cudaSuccess) return err;
     constexpr int CL = PAIR ? 2 * C : C;
     note_launches(1);

@@ -1354,9 +1354,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_logits_bwd_chosen_kernel
 
 template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
 cudaError_t launch_route(const RouteArgs& a, int grid, cudaStream_t st) {
-    auto kern = route_logits_kernel<VPT, SOFTMAX, WARPS, SMALL>;
+    constexpr auto kern = route_logits_kernel<VPT, SOFTMAX, WARPS, SMALL>;
     constexpr size_t smem = WARPS * sizeof(WarpMem) + (kMaxExperts + 4) * sizeof(int);
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem<kern>(smem);
     if (err != cudaSuccess) return err;
     note_launches(1);
     return launch_after(kern, dim3((unsigned)grid), WARPS * 32, smem, SMALL ? grid : 1, st, a);
@@ -1382,9 +1382,9 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
 
 template <int NCH, bool SOFTMAX, bool SCORED>
 cudaError_t launch_quad_s(const RouteArgs& a, int num_sms, cudaStream_t st) {
-    auto kern = route_logits_quad_kernel<NCH, SOFTMAX, SCORED>;
+    constexpr auto kern = route_logits_quad_kernel<NCH, SOFTMAX, SCORED>;
     constexpr size_t smem = kQuadWarps * sizeof(WarpMem) + 8 * NCH * sizeof(float4) + kMaxExperts * sizeof(int);
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem<kern>(smem);
     if (err != cudaSuccess) return err;
     note_launches(2);
     err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);

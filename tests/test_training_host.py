@@ -243,13 +243,17 @@ def test_saved_act_tensors_are_checked():
         moe.moe_swiglu_backward_saved(moe.saved_acts(buf), sh, moe.MOE_ROUTED, FAKE, FAKE, FAKE, FAKE, None, FAKE, stream=0)
     with pytest.raises(moe.MoEError, match="contiguous"):
         moe.saved_acts({"a": torch.empty((4, 8), dtype=torch.uint8).t()})
-    s = moe.saved_acts({n: FAKE for n, _ in moe.MoESavedActs._fields_})
-    s.device = 0
-    rows = dict(a=sh.T * sh.k * sh.I, g_scale=sh.T * sh.k * sh.I // 32, sa=sh.T * sh.Is, sg_scale=sh.T * sh.Is // 32)
-    for name, need in rows.items():  # a buffer of one byte less than its rows
-        s.sizes = {name: need - 1}
-        part = moe.MOE_SHARED if name.startswith("s") else moe.MOE_ROUTED
-        with pytest.raises(moe.MoEError, match=name):
-            moe.moe_swiglu_backward_saved(s, sh, part, FAKE, FAKE, FAKE, FAKE, None, FAKE, stream=0)
-        with pytest.raises(moe.MoEError, match=name):
-            moe.moe_ffn_up_save(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, sh, FAKE, FAKE, s, stream=0)
+    # buffers of a smaller layer, taken for ones on a device
+    small = moe.saved_acts(moe.saved_act_buffers(shape(I=128, T=127), "cpu"))
+    small.device = 0
+    for part in (moe.MOE_SHARED, moe.MOE_ROUTED):
+        with pytest.raises(moe.MoEError, match="need"):
+            moe.moe_swiglu_backward_saved(small, sh, part, FAKE, FAKE, FAKE, FAKE, None, FAKE, stream=0)
+    with pytest.raises(moe.MoEError, match="need"):
+        moe.moe_ffn_up_save(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, sh, FAKE, FAKE, small, stream=0)
+    # one short scale buffer
+    buf["sg_scale"] = buf["sg_scale"][:-1]
+    short = moe.saved_acts(buf)
+    short.device = 0
+    with pytest.raises(moe.MoEError, match="need"):
+        moe.moe_swiglu_backward_saved(short, sh, moe.MOE_SHARED, FAKE, None, None, FAKE, None, None, stream=0)
