@@ -815,9 +815,9 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
     route_logits_quad_kernel(const __grid_constant__ RouteArgs a) {
     static_assert(!(SOFTMAX && SCORED), "closer values would need the 64-bit sum");
     constexpr int N = 4 * NCH;
-    constexpr uint32_t kTag = N - 1;
-    // the rounding of v and its low bits, (1 + 2 (N - 1)) 2^-24 < N 2^-23
-    constexpr float kTagErr = N * 0x1p-23f, kLogitErr = 0x1p-30f;
+    constexpr uint32_t kTag = N <= 8 ? 7 : N <= 16 ? 15 : 31;  // low bits that name the register
+    // the rounding of v and its low bits, (1 + 2 kTag) 2^-24 < (kTag + 1) 2^-23
+    constexpr float kTagErr = (kTag + 1) * 0x1p-23f, kLogitErr = 0x1p-30f;
     constexpr float kSaturated = 20.0f, kUnderflow = -600.0f;
     extern __shared__ __align__(16) uint8_t smem[];
     WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
@@ -870,28 +870,25 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
             const int c = r + 8 * i;
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[4 * i + j] = kMasked;
-            if (8 * i < chunks) {
-                if (vec) {
-                    if (c < chunks) {
-                        const float4 x = *reinterpret_cast<const float4*>(row + 4 * c);
-                        v[4 * i] = x.x;
-                        v[4 * i + 1] = x.y;
-                        v[4 * i + 2] = x.z;
-                        v[4 * i + 3] = x.w;
-                    }
-                } else {
-                    const int g = group_of >> (4 * i) & 15, off = 4 * (c - g * a.run_chunks);
-                    const float* p = row + g * a.run + off;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (c < chunks && off + j < a.run) v[4 * i + j] = p[j];
+            if (vec) {
+                if (c < chunks) {
+                    const float4 x = *reinterpret_cast<const float4*>(row + 4 * c);
+                    v[4 * i] = x.x;
+                    v[4 * i + 1] = x.y;
+                    v[4 * i + 2] = x.z;
+                    v[4 * i + 3] = x.w;
                 }
+            } else {
+                const int g = group_of >> (4 * i) & 15, off = 4 * (c - g * a.run_chunks);
+                const float* p = row + g * a.run + off;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c < chunks && off + j < a.run) v[4 * i + j] = p[j];
             }
         }
         float nf = 0.0f;  // NaN where a logit is not finite
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (8 * (j / 4) < chunks) nf = fmaf(v[j], 0.0f, nf);
+        for (int j = 0; j < N; ++j) nf = fmaf(v[j], 0.0f, nf);
         const bool special = __any_sync(kFull, nf != nf);
         unsigned masked = 0u;
         bool again = false;
@@ -906,21 +903,16 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
         if (SOFTMAX && !a.o.renormalize) {
             m = v[0];
 #pragma unroll
-            for (int j = 1; j < N; ++j)
-                if (8 * (j / 4) < chunks) m = fmaxf(m, v[j]);  // NaN drops out
+            for (int j = 1; j < N; ++j) m = fmaxf(m, v[j]);  // NaN drops out
             m = max8(m);
             again |= !(m > kLow);
             float part = 0.0f;
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (8 * (j / 4) >= chunks) continue;
-                part += ex2_fast((v[j] - m) * kLog2e);
-            }
+            for (int j = 0; j < N; ++j) part += ex2_fast((v[j] - m) * kLog2e);
             top = rcp_fast(fmaxf(sum8(part), 1e-30f));
         }
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            if (8 * i >= chunks) continue;
             float b[4] = {};
             if (SCORED) *reinterpret_cast<float4*>(b) = bias[r + 8 * i];
 #pragma unroll
@@ -937,7 +929,6 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
         }
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            if (8 * i >= chunks) continue;
             order(v[4 * i], v[4 * i + 1]);
             order(v[4 * i + 2], v[4 * i + 3]);
             order(v[4 * i], v[4 * i + 2]);
@@ -1025,7 +1016,6 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
         float x[4];
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            if (i > 0 && 8 * i >= chunks) continue;
             const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : neg_inf();
             if (i == 0) {
 #pragma unroll
@@ -1058,7 +1048,6 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
                 float y = kMasked;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    if (8 * i >= chunks) continue;
                     const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : neg_inf();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -1094,7 +1083,6 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
                 int all = 0;  // values that may be among the k
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    if (8 * i >= chunks) continue;
                     const float out = kept >> (group_of >> (4 * i) & 15) & 1u ? 0.0f : neg_inf();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) all += v[4 * i + j] + out >= cut;
@@ -1433,8 +1421,7 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
     const bool scored = bias || (grouped && o.group_top == 2);
     const bool quad = T >= (scored ? 13 : 3) * E && T > 128 && !(scored && o.softmax) && k <= 8 &&
                       (!grouped || o.groups <= 8) && chunks <= 64;
-    int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
-    if (quad) vpt = chunks <= 16 ? 2 : chunks <= 32 ? 4 : 8;  // chunks per lane; then E <= 32 vpt as well
+    const int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
     const int per = E / o.groups, whole = per % vpt == 0 ? per / vpt : 0;
     int lanes = whole > 0 && (whole & (whole - 1)) == 0 ? whole : 1;
     if (whole != lanes)
@@ -1447,10 +1434,15 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
     const RouteArgs a{logits, bias,   T,      E, k, per, (65536 + per - 1) / per, lanes,
                       direct, leaders, run, run_chunks, chunks, (65536 + run_chunks - 1) / run_chunks, o, idx, w, counts,
                       status};
-    if (quad)
-        return vpt == 2   ? launch_quad<2>(a, scored, num_sms, st)
-               : vpt == 4 ? launch_quad<4>(a, scored, num_sms, st)
-                          : launch_quad<8>(a, scored, num_sms, st);
+    if (quad) switch ((chunks + 7) / 8) {  // chunks per lane
+            case 1:
+            case 2: return launch_quad<2>(a, scored, num_sms, st);
+            case 3: return launch_quad<3>(a, scored, num_sms, st);
+            case 4: return launch_quad<4>(a, scored, num_sms, st);
+            case 5: return launch_quad<5>(a, scored, num_sms, st);
+            case 6: return launch_quad<6>(a, scored, num_sms, st);
+            default: return launch_quad<8>(a, scored, num_sms, st);
+        }
     switch (vpt) {
         case 1: return launch_route_v<1>(a, num_sms, st);
         case 2: return launch_route_v<2>(a, num_sms, st);
