@@ -4,16 +4,16 @@
 // DeepSeekMoE sketch: softmax gating), with sigmoid or softmax scores and the
 // choice limited to the best groups of experts.
 //
-// Forward, one warp per token:
+// Forward, one warp per token, or per four tokens of a batch:
 //   s = sigmoid(z) or softmax(z);  v = s + bias;
 //   group value = sum of the group's 1 or 2 largest v; the top_groups best
 //   groups are kept (ties: lower group); the k largest v of the kept groups
 //   in descending order (ties: lower expert);  w = scale s / (sum of the k s).
-// v is defined in 64 bits.  The kernel forms it in 32 and bounds the error:
+// v is defined in 64 bits.  The kernels form it in 32 and bound the error:
 // where two values whose order matters are closer than the bound, the values
 // concerned are formed again in 64 bits.
 //
-// Backward, one warp per token, for the choice made:  with G = scale dw,
+// Backward, one warp per token or several, for the choice made:  with G = scale dw,
 //   renormalised:  dz_j = p_j (G_j - sum G p) (sigmoid: times 1 - s_j), p the
 //     chosen scores' shares, whatever the other experts' logits are;
 //   as scored:     ds_j += G_j;
@@ -784,7 +784,12 @@ __device__ __forceinline__ T sum8(T v) {
     return v;
 }
 
-constexpr int kQuadWarps = 16, kQuadCtas = 2;  // CTAs per SM
+// Warps per CTA and CTAs per SM: 80 registers for the 32 values of a lane, 64
+// for fewer (8192 x 256 sigmoid groups: 8.7 us, with 64 registers 9.3; 32768 x
+// 160 softmax groups: 12.1 us, with 80 13.4).  More and smaller CTAs add up
+// more counts (one atomic per expert and CTA).
+constexpr int kQuadCtas = 2;
+__host__ __device__ constexpr int quad_warps(int nch) { return nch == 8 ? 12 : 16; }
 constexpr int kQuadTops = 81;  // float2 per token: 64 chunks, one gap per run, on shifting banks
 static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 
@@ -805,28 +810,27 @@ static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 // per lane (0.6% of the tokens of 256 normal logits with biases).  What is left
 // (closer still, NaN, +inf, too few experts) is done by route_token64, 6 us.
 //
-// Issue bound: 32768 x 256 sigmoid tokens with groups execute 466 instructions
-// each and take 22.4 us (a warp per token 34.6), 32768 x 160 softmax tokens 17.3
-// (36.1); 8192 x 256 10.2 (14.4).  16 warps per CTA, two CTAs per SM with 64
-// registers: three CTAs of 8 warps with 80 took 24.9, 20.0 and 9.9 us, one of 32
-// 22.3, 16.6 and 10.3.  Every CTA adds its counts with E atomics, so few are best.
+// Issue bound (figures with the logits in L2): 32768 x 160 softmax tokens in
+// groups execute 250 instructions each and take 12.1 us (a warp per token 36;
+// the logits at the copy rate 3.3), 32768 x 256 sigmoid tokens in groups 19.8
+// (34.6; 5.2), 8192 x 256 8.8 (14.4; 1.3), of which about 3 are the two launches.
 template <int NCH, bool SOFTMAX, bool SCORED>
-__global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
+__global__ void __launch_bounds__(quad_warps(NCH) * 32, kQuadCtas)
     route_logits_quad_kernel(const __grid_constant__ RouteArgs a) {
     static_assert(!(SOFTMAX && SCORED), "closer values would need the 64-bit sum");
-    constexpr int N = 4 * NCH;
+    constexpr int N = 4 * NCH, WARPS = quad_warps(NCH);
     constexpr uint32_t kTag = N <= 8 ? 7 : N <= 16 ? 15 : 31;  // low bits that name the register
     // the rounding of v and its low bits, (1 + 2 kTag) 2^-24 < (kTag + 1) 2^-23
     constexpr float kTagErr = (kTag + 1) * 0x1p-23f, kLogitErr = 0x1p-30f;
     constexpr float kSaturated = 20.0f, kUnderflow = -600.0f;
     extern __shared__ __align__(16) uint8_t smem[];
     WarpMem& wm = reinterpret_cast<WarpMem*>(smem)[threadIdx.x >> 5];
-    float4* bias = reinterpret_cast<float4*>(smem + kQuadWarps * sizeof(WarpMem));  // by chunk; masked: kMasked
+    float4* bias = reinterpret_cast<float4*>(smem + WARPS * sizeof(WarpMem));  // by chunk; masked: kMasked
     int* hist = reinterpret_cast<int*>(bias + 8 * NCH);
     const int tid = threadIdx.x, lane = tid & 31, r = lane & 7, first_lane = lane & 24;
     const int E = a.E, k = a.k, chunks = a.chunks;
     if (SCORED)
-        for (int i = tid; i < 8 * N; i += kQuadWarps * 32) {
+        for (int i = tid; i < 8 * N; i += WARPS * 32) {
             const int c = i >> 2, g = c * a.chunk_inv >> 16, off = 4 * (c - g * a.run_chunks) + (i & 3);
             float b = kMasked;
             if (c < chunks && off < a.run) {
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
             }
             reinterpret_cast<float*>(bias)[i] = b;
         }
-    for (int e = tid; e < E; e += kQuadWarps * 32) hist[e] = 0;
+    for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
     __syncthreads();
 
     const bool vec = (a.run & 3) == 0, grouped = a.o.top_groups < a.o.groups;
@@ -860,7 +864,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
     };
 
     const int quads = (a.T - 1) / 4 + 1;
-    for (int q = (tid >> 5) * gridDim.x + blockIdx.x; q < quads; q += gridDim.x * kQuadWarps) {
+    for (int q = (tid >> 5) * gridDim.x + blockIdx.x; q < quads; q += gridDim.x * WARPS) {
         const int t = 4 * q + (lane >> 3);
         const bool in = t < a.T;  // else the last token once more, not stored
         const float* row = a.logits + (size_t)(in ? t : a.T - 1) * E;
@@ -1136,7 +1140,7 @@ __global__ void __launch_bounds__(kQuadWarps * 32, kQuadCtas)
     }
     __syncthreads();
     grid_dependency_wait();  // the counters are clear
-    for (int e = tid; e < E; e += kQuadWarps * 32)
+    for (int e = tid; e < E; e += WARPS * 32)
         if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
 }
 
@@ -1371,16 +1375,17 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
 template <int NCH, bool SOFTMAX, bool SCORED>
 cudaError_t launch_quad_s(const RouteArgs& a, int num_sms, cudaStream_t st) {
     constexpr auto kern = route_logits_quad_kernel<NCH, SOFTMAX, SCORED>;
-    constexpr size_t smem = kQuadWarps * sizeof(WarpMem) + 8 * NCH * sizeof(float4) + kMaxExperts * sizeof(int);
+    constexpr int WARPS = quad_warps(NCH);
+    constexpr size_t smem = WARPS * sizeof(WarpMem) + 8 * NCH * sizeof(float4) + kMaxExperts * sizeof(int);
     cudaError_t err = allow_smem<kern>(smem);
     if (err != cudaSuccess) return err;
     note_launches(2);
     err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);
     if (err != cudaSuccess) return err;
     // over all SMs first, then more warps of each: rounds of one quad per warp of an SM's CTA
-    const int quads = (a.T - 1) / 4 + 1, rounds = (quads - 1) / (kQuadWarps * num_sms) + 1;
+    const int quads = (a.T - 1) / 4 + 1, rounds = (quads - 1) / (WARPS * num_sms) + 1;
     const int grid = quads < num_sms ? quads : (rounds < kQuadCtas ? rounds : kQuadCtas) * num_sms;
-    return launch_after(kern, dim3((unsigned)grid), kQuadWarps * 32, smem, 1, st, a);
+    return launch_after(kern, dim3((unsigned)grid), WARPS * 32, smem, 1, st, a);
 }
 
 template <int NCH>
@@ -1412,14 +1417,15 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
     if (T == 0) return cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)E, st);
     const bool grouped = o.top_groups < o.groups;
     const int run = grouped ? E / o.groups : E, run_chunks = (run + 3) / 4, chunks = run_chunks * (E / run);
-    // Four tokens per warp, where there are enough of them: a quad takes longer
-    // than a token (us for 1024, 2048, 4096 tokens, a warp per token against four:
-    // 256 experts sigmoid with bias 5.5 6.1 9.1, 7.8 7.8 8.0, 128 experts 5.0 6.3 7.4,
-    // 5.5 5.6 5.8; without bias, 256 experts softmax 6.6 7.7 9.2, 6.1 6.4 6.7, 64
-    // experts 6.0 6.2 8.1, 3.9 4.1 4.3).  Softmax with a bias or sums of two stays
-    // with a warp per token: its close values need the sum in 64 bits.
+    // Four tokens per warp for batches (us for 512, 1024, 2048, 3500 tokens, a
+    // warp per token against four: 256 experts sigmoid with bias 5.4 5.4 6.3 8.2,
+    // 5.3 6.1 6.0 6.4, in groups 5.8 7.3 7.5 8.7, 6.1 6.4 6.5 6.8; 256 experts softmax
+    // 4.5 6.8 7.7 8.7, 4.6 4.9 5.1 5.5; 64 experts softmax 6.1 6.1 6.1 7.4, 3.9 4.0 4.0
+    // 4.0).  Softmax with a bias or sums of two stays with a warp per token: its
+    // close values need the sum in 64 bits, and a quad waits 6 us for that (4096 x
+    // 256: 13.0 us against 10.3).
     const bool scored = bias || (grouped && o.group_top == 2);
-    const bool quad = T >= (scored ? 13 : 3) * E && T > 128 && !(scored && o.softmax) && k <= 8 &&
+    const bool quad = T > 128 && !(scored && o.softmax) && k <= 8 &&
                       (!grouped || o.groups <= 8) && chunks <= 64;
     const int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
     const int per = E / o.groups, whole = per % vpt == 0 ? per / vpt : 0;
