@@ -29,6 +29,8 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxK = 16;
+// Tokens, and CTAs, of a batch that one cluster takes
+constexpr int kSmallTokens = 128, kSmallCtas = 8;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ double neg_inf64() { return __longlong_as_double(0xfff0000000000000ll); }
@@ -229,8 +231,8 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return r;
 }
 
-// Issue bound: one token costs a few hundred warp instructions whatever its
-// k, and its row only E floats.  So the scores that only decide the choice use
+// Issue bound: one token costs 500 to 700 warp instructions whatever its k,
+// and its row only E floats.  So the scores that only decide the choice use
 // the hardware's exponential and reciprocal (2 instructions each), and the
 // accurate ones are left to the k chosen, one per lane.  A value's low three
 // bits are replaced by its register's number j, so that values alone are compared and moved.  Every lane sorts its four best; k + 1
@@ -607,8 +609,29 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
             if (bad) report(a.status, kStDeviceCheck);
 }
 
-// SMALL: one cluster takes the batch and adds its CTAs' counts itself;
-// otherwise counts were cleared by the kernel before this one on the stream.
+// The CTA's counts to all.  SMALL: one cluster takes the batch and adds its
+// CTAs' counts itself; otherwise counts were cleared by the kernel before this
+// one on the stream.
+template <int WARPS, bool SMALL>
+__device__ __forceinline__ void finish_counts(const RouteArgs& a, const int* hist, int tid) {
+    const int E = a.E;
+    if (SMALL) {
+        cluster_sync_all();  // every CTA's counts are in
+        const unsigned n_ctas = gridDim.x;
+        for (int e = blockIdx.x * WARPS * 32 + tid; e < E; e += n_ctas * WARPS * 32) {
+            int c = 0;
+            for (unsigned r = 0; r < n_ctas; ++r) c += ld_cluster_i32(mapa_shared(smem_u32(hist + e), r));
+            a.counts[e] = c;
+        }
+        cluster_sync_all();  // no CTA leaves while its counts are read
+    } else {
+        __syncthreads();
+        grid_dependency_wait();  // the counters are clear
+        for (int e = tid; e < E; e += WARPS * 32)
+            if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
+    }
+}
+
 template <int VPT, bool SOFTMAX, int WARPS, bool SMALL>
 __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     route_logits_kernel(const __grid_constant__ RouteArgs a) {
@@ -638,21 +661,7 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
             asm volatile("prefetch.global.L1 [%0];" ::"l"(a.logits + (size_t)t_next * E + 32 * lane));
         route_token<VPT, SOFTMAX>(a, wm, hist, b, odd, t, lane);
     }
-    if (SMALL) {
-        cluster_sync_all();  // every CTA's counts are in
-        const unsigned n_ctas = gridDim.x;
-        for (int e = blockIdx.x * WARPS * 32 + tid; e < E; e += n_ctas * WARPS * 32) {
-            int c = 0;
-            for (unsigned r = 0; r < n_ctas; ++r) c += ld_cluster_i32(mapa_shared(smem_u32(hist + e), r));
-            a.counts[e] = c;
-        }
-        cluster_sync_all();  // no CTA leaves while its counts are read
-    } else {
-        __syncthreads();
-        grid_dependency_wait();  // the counters are clear
-        for (int e = tid; e < E; e += WARPS * 32)
-            if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
-    }
+    finish_counts<WARPS, SMALL>(a, hist, tid);
 }
 
 // ---- four tokens per warp ----
@@ -784,12 +793,14 @@ __device__ __forceinline__ T sum8(T v) {
     return v;
 }
 
-// Warps per CTA and CTAs per SM: 80 registers for the 32 values of a lane, 64
+// Warps per CTA and CTAs per SM of a batch: 80 registers for the 32 values of a lane, 64
 // for fewer (8192 x 256 sigmoid groups: 8.7 us, with 64 registers 9.3; 32768 x
 // 160 softmax groups: 12.1 us, with 80 13.4).  More and smaller CTAs add up
-// more counts (one atomic per expert and CTA).
+// more counts (one atomic per expert and CTA).  A small batch: one cluster of as
+// many CTAs as it fills, one up to 32 tokens (the cluster's barrier and reads
+// cost 0.8 us; 4 warps per CTA 0.6 more at 32, 16 warps 0.2 to 1.5 at 64 to 128).
 constexpr int kQuadCtas = 2;
-__host__ __device__ constexpr int quad_warps(int nch) { return nch == 8 ? 12 : 16; }
+__host__ __device__ constexpr int quad_warps(int nch, bool small) { return small ? 8 : nch == 8 ? 12 : 16; }
 constexpr int kQuadTops = 81;  // float2 per token: 64 chunks, one gap per run, on shifting banks
 static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 
@@ -814,11 +825,11 @@ static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 // groups execute 250 instructions each and take 12.1 us (a warp per token 36;
 // the logits at the copy rate 3.3), 32768 x 256 sigmoid tokens in groups 19.8
 // (34.6; 5.2), 8192 x 256 8.8 (14.4; 1.3), of which about 3 are the two launches.
-template <int NCH, bool SOFTMAX, bool SCORED>
-__global__ void __launch_bounds__(quad_warps(NCH) * 32, kQuadCtas)
+template <int NCH, bool SOFTMAX, bool SCORED, bool SMALL>
+__global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuadCtas)
     route_logits_quad_kernel(const __grid_constant__ RouteArgs a) {
     static_assert(!(SOFTMAX && SCORED), "closer values would need the 64-bit sum");
-    constexpr int N = 4 * NCH, WARPS = quad_warps(NCH);
+    constexpr int N = 4 * NCH, WARPS = quad_warps(NCH, SMALL);
     constexpr uint32_t kTag = N <= 8 ? 7 : N <= 16 ? 15 : 31;  // low bits that name the register
     // the rounding of v and its low bits, (1 + 2 kTag) 2^-24 < (kTag + 1) 2^-23
     constexpr float kTagErr = (kTag + 1) * 0x1p-23f, kLogitErr = 0x1p-30f;
@@ -829,6 +840,7 @@ __global__ void __launch_bounds__(quad_warps(NCH) * 32, kQuadCtas)
     int* hist = reinterpret_cast<int*>(bias + 8 * NCH);
     const int tid = threadIdx.x, lane = tid & 31, r = lane & 7, first_lane = lane & 24;
     const int E = a.E, k = a.k, chunks = a.chunks;
+    if (SMALL) grid_dependency_wait();
     if (SCORED)
         for (int i = tid; i < 8 * N; i += WARPS * 32) {
             const int c = i >> 2, g = c * a.chunk_inv >> 16, off = 4 * (c - g * a.run_chunks) + (i & 3);
@@ -1138,10 +1150,7 @@ __global__ void __launch_bounds__(quad_warps(NCH) * 32, kQuadCtas)
             route_token64<SOFTMAX>(a, wm, hist, 4 * q + which, lane);
         }
     }
-    __syncthreads();
-    grid_dependency_wait();  // the counters are clear
-    for (int e = tid; e < E; e += WARPS * 32)
-        if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
+    finish_counts<WARPS, SMALL>(a, hist, tid);
 }
 
 // Clears the counters.  The routing kernel starts beside it, once everything
@@ -1356,8 +1365,12 @@ cudaError_t launch_route(const RouteArgs& a, int grid, cudaStream_t st) {
 
 template <int VPT>
 cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
-    constexpr int kSmallWarps = 16, kSmallCtas = 8;
-    if (a.T <= kSmallWarps * kSmallCtas) {  // a token per warp of one cluster
+    // A token per warp of one cluster, of one CTA up to 8 tokens (3.8 us; a cluster
+    // of 8 4.8).  From 9 tokens on the launch that clears the counts and the other
+    // form take as long or less on the device (64 tokens 5.6 us against 6.0), but
+    // the host needs 2 us more for a second launch.
+    constexpr int kSmallWarps = kSmallTokens / kSmallCtas;
+    if (a.T <= kSmallTokens) {
         const int grid = a.T <= 8 ? 1 : kSmallCtas;
         if (a.T <= 8 * kSmallCtas)
             return a.o.softmax ? launch_route<VPT, true, 8, true>(a, grid, st)
@@ -1372,27 +1385,39 @@ cudaError_t launch_route_v(const RouteArgs& a, int num_sms, cudaStream_t st) {
     return a.o.softmax ? launch_route<VPT, true, 8, false>(a, grid, st) : launch_route<VPT, false, 8, false>(a, grid, st);
 }
 
-template <int NCH, bool SOFTMAX, bool SCORED>
+template <int NCH, bool SOFTMAX, bool SCORED, bool SMALL>
 cudaError_t launch_quad_s(const RouteArgs& a, int num_sms, cudaStream_t st) {
-    constexpr auto kern = route_logits_quad_kernel<NCH, SOFTMAX, SCORED>;
-    constexpr int WARPS = quad_warps(NCH);
+    constexpr auto kern = route_logits_quad_kernel<NCH, SOFTMAX, SCORED, SMALL>;
+    constexpr int WARPS = quad_warps(NCH, SMALL);
     constexpr size_t smem = WARPS * sizeof(WarpMem) + 8 * NCH * sizeof(float4) + kMaxExperts * sizeof(int);
     cudaError_t err = allow_smem<kern>(smem);
     if (err != cudaSuccess) return err;
+    const int quads = (a.T - 1) / 4 + 1;
+    if (SMALL) {
+        const int grid = (quads - 1) / WARPS + 1;
+        note_launches(1);
+        return launch_after(kern, dim3((unsigned)grid), WARPS * 32, smem, grid, st, a);
+    }
     note_launches(2);
     err = launch_after(clear_counts_kernel, dim3(1), 256, 0, 1, st, a.counts, a.E);
     if (err != cudaSuccess) return err;
     // over all SMs first, then more warps of each: rounds of one quad per warp of an SM's CTA
-    const int quads = (a.T - 1) / 4 + 1, rounds = (quads - 1) / (WARPS * num_sms) + 1;
+    const int rounds = (quads - 1) / (WARPS * num_sms) + 1;
     const int grid = quads < num_sms ? quads : (rounds < kQuadCtas ? rounds : kQuadCtas) * num_sms;
     return launch_after(kern, dim3((unsigned)grid), WARPS * 32, smem, 1, st, a);
 }
 
 template <int NCH>
 cudaError_t launch_quad(const RouteArgs& a, bool scored, int num_sms, cudaStream_t st) {
-    if (scored) return launch_quad_s<NCH, false, true>(a, num_sms, st);
-    return a.o.softmax ? launch_quad_s<NCH, true, false>(a, num_sms, st)
-                       : launch_quad_s<NCH, false, false>(a, num_sms, st);
+    const bool small = a.T <= kSmallTokens;
+    if (scored)
+        return small ? launch_quad_s<NCH, false, true, true>(a, num_sms, st)
+                     : launch_quad_s<NCH, false, true, false>(a, num_sms, st);
+    if (a.o.softmax)
+        return small ? launch_quad_s<NCH, true, false, true>(a, num_sms, st)
+                     : launch_quad_s<NCH, true, false, false>(a, num_sms, st);
+    return small ? launch_quad_s<NCH, false, false, true>(a, num_sms, st)
+                 : launch_quad_s<NCH, false, false, false>(a, num_sms, st);
 }
 
 template <int VPT>
@@ -1417,15 +1442,16 @@ cudaError_t launch_route_logits(const float* logits, const float* bias, int T, i
     if (T == 0) return cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)E, st);
     const bool grouped = o.top_groups < o.groups;
     const int run = grouped ? E / o.groups : E, run_chunks = (run + 3) / 4, chunks = run_chunks * (E / run);
-    // Four tokens per warp for batches (us for 512, 1024, 2048, 3500 tokens, a
-    // warp per token against four: 256 experts sigmoid with bias 5.4 5.4 6.3 8.2,
-    // 5.3 6.1 6.0 6.4, in groups 5.8 7.3 7.5 8.7, 6.1 6.4 6.5 6.8; 256 experts softmax
-    // 4.5 6.8 7.7 8.7, 4.6 4.9 5.1 5.5; 64 experts softmax 6.1 6.1 6.1 7.4, 3.9 4.0 4.0
-    // 4.0).  Softmax with a bias or sums of two stays with a warp per token: its
-    // close values need the sum in 64 bits, and a quad waits 6 us for that (4096 x
-    // 256: 13.0 us against 10.3).
+    // Four tokens per warp (us for 8, 32, 64, 128, 512, 1024, 2048, 3500 tokens, a
+    // warp per token against four: 256 experts sigmoid with bias in groups 3.8 5.5 5.7
+    // 6.2 5.8 7.3 7.5 8.7, 4.2 5.7 6.3 6.5 6.1 6.4 6.5 6.8; 256 experts softmax 3.4 4.2 4.3
+    // 5.0 4.5 6.8 7.7 8.7, 3.5 3.8 4.7 4.7 4.6 4.9 5.1 5.5; 64 experts sigmoid with bias 2.6
+    // 3.4 4.3 4.5 4.8 4.8 5.0 6.2, 2.8 3.0 4.3 4.3 4.4 4.5 4.5 4.7; 64 experts softmax 2.7
+    // 3.4 3.5 6.9 6.1 6.1 6.1 7.4, 2.6 2.8 3.5 3.6 3.9 4.0 4.0 4.0).  Softmax with a bias or
+    // sums of two stays with a warp per token: its close values need the sum in
+    // 64 bits, and a quad waits 6 us for that (4096 x 256: 13.0 us against 10.3).
     const bool scored = bias || (grouped && o.group_top == 2);
-    const bool quad = T > 128 && !(scored && o.softmax) && k <= 8 &&
+    const bool quad = T > (scored && chunks > 32 ? kSmallTokens : 8) && !(scored && o.softmax) && k <= 8 &&
                       (!grouped || o.groups <= 8) && chunks <= 64;
     const int vpt = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;  // experts per lane
     const int per = E / o.groups, whole = per % vpt == 0 ? per / vpt : 0;
