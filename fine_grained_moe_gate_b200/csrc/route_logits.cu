@@ -331,7 +331,12 @@ __device__ __forceinline__ float cut_of(float best, float abs_err, float rel_err
 
 // The general way to the k + 1 best: all values of the kept groups (bit g LG
 // of kept) from cut up, compacted and ranked by counting.  Returns whether two
-// of them are equal; n: how many.
+// of them are equal; n: how many.  More than kManyCandidates (rows of equal
+// values) are not ranked: route_token64's k rounds are shorter then (8192 rows of
+// 256 equal values: 35 us, by ranking 452).
+constexpr int kManyCandidates = 48;
+template <bool SOFTMAX>
+__device__ __noinline__ void route_token64(const RouteArgs& a, WarpMem& wm, int* hist, int t, int lane);
 template <int VPT>
 __device__ __noinline__ bool rank_candidates(const RouteArgs& a, const float (&v)[VPT], unsigned kept, int LG, float cut,
                                              WarpMem& wm, int lane, int& n) {
@@ -348,6 +353,7 @@ __device__ __noinline__ bool rank_candidates(const RouteArgs& a, const float (&v
         if (lane >= o) pos += x;
     }
     n = __shfl_sync(kFull, pos, 31);
+    if (n > kManyCandidates) return true;
     pos -= __popc(in);
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
@@ -584,6 +590,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
             if (pairs || __any_sync(kFull, close)) {
                 if (((pairs >> (k - 1)) & 1u) || __any_sync(kFull, close)) {  // who is among the k, too
                     if (!ranked) rank_candidates<VPT>(a, v, kept, LG, cut_of(best, abs_err, rel_err), wm, lane, n);
+                    if (n > kManyCandidates) return route_token64<SOFTMAX>(a, wm, hist, t, lane);
                     __syncwarp();
                     sort_candidates64(a, row, wm, n, lane);
                     e = live ? wm.place[lane] : -1;
@@ -670,9 +677,8 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
 __device__ __noinline__ double sigmoid64(float z, float b) { return 1.0 / (1.0 + exp(-(double)z)) + (double)b; }
 
 // One token by one warp with every value in 64 bits: k rounds of the largest.
-// Rarely called, so its instructions come from memory: loops instead of
-// unrolled code (the 32-bit choice with its 64-bit repairs, unrolled, took 5
-// us from a cold start).
+// 6 us for one token of 256 (11700 cycles, most of them FP64 and 64-bit
+// compares in dependence), but 8192 rows of equal values take 35 us in all.
 template <bool SOFTMAX>
 __device__ __noinline__ void route_token64(const RouteArgs& a, WarpMem& wm, int* hist, int t, int lane) {
     constexpr int N = kMaxExperts / 32;

@@ -602,3 +602,19 @@ def test_small_batches_at_each_form(T):
             z[:, 5] = float("-inf")
         check_route(z, bias if with_bias else None, k, o)
     check_status()
+
+
+@pytest.mark.parametrize("T", [5, 100, 700])
+def test_rows_of_equal_values(T):
+    """Every expert a candidate: zeros (a padded batch), a coarse grid, rows of either kind in turn."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    for E, k in ((256, 8), (256, 12), (60, 4), (96, 16)):
+        z = torch.randint(-1, 2, (T, E), generator=g, device=DEV).float()
+        z[::2] = 0.0
+        z[1::4] += torch.randn((z[1::4].shape), generator=g, device=DEV)
+        bias = torch.full((E,), 0.125, device=DEV)
+        for o in (ot.Opts(score="softmax"), ot.Opts(), ot.Opts(groups=4, top_groups=3, group_top=2),
+                  ot.Opts(score="softmax", groups=4, top_groups=2, group_top=2, renormalize=False)):
+            check_route(z, bias, k, o)
+            check_route(z, None, k, o)
+    check_status()
