@@ -29,7 +29,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxK = 16;
-// Tokens, and CTAs, of a batch that one cluster takes
+// Tokens, and CTAs, of a batch that one cluster takes.  A second launch costs the
+// host 2 us; on the device the cluster's barriers and reads take 0.3 us longer at
+// 128 tokens, 0.6 to 0.9 at 136 to 256.
 constexpr int kSmallTokens = 128, kSmallCtas = 8;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -235,11 +237,11 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // and its row only E floats.  So the scores that only decide the choice use
 // the hardware's exponential and reciprocal (2 instructions each), and the
 // accurate ones are left to the k chosen, one per lane.  A value's low three
-// bits are replaced by its register's number j, so that values alone are compared and moved.  Every lane sorts its four best; k + 1
-// warp maxima take the best values in descending order, the lane that owns one
-// moves its next up.  Where a lane would need its fifth, or two values are
-// equal, all values from the threshold found up are compacted and ranked by
-// counting instead.
+// bits are replaced by its register's number j, so that values alone are
+// compared and moved.  Every lane sorts its four best; k + 1 warp maxima take the
+// best values in descending order, the lane that owns one moves its next up.
+// Where a lane would need its fifth, or two values are equal, all values from the
+// threshold found up are compacted and ranked by counting instead.
 //
 // Error bounds, u = 2^-24.  e = 2^(x log2 e): the product's rounding |x| u,
 // the hardware's 2 ulp (4u), 1 + e and its reciprocal (3u), for softmax the
@@ -585,7 +587,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
                 }
             }
             const float next = __shfl_down_sync(kFull, mine, 1);
-            const bool unclear = live && lane + 1 < n && !(mine - next > abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f);
+            const float gap = abs_err + rel_err * (fabsf(mine) + fabsf(next)) + 1e-37f;
+            const bool unclear = live && lane + 1 < n && !(mine - next > gap);
             const unsigned pairs = __ballot_sync(kFull, unclear);
             if (pairs || __any_sync(kFull, close)) {
                 if (((pairs >> (k - 1)) & 1u) || __any_sync(kFull, close)) {  // who is among the k, too
@@ -774,7 +777,9 @@ __device__ __noinline__ void route_token64(const RouteArgs& a, WarpMem& wm, int*
     if (a.o.renormalize)
         wt = k <= 8 ? chosen_share<8>(z, live, SOFTMAX) : chosen_share<16>(z, live, SOFTMAX);
     else
-        wt = !live ? 0.0f : SOFTMAX ? (z == m ? 1.0f : expf(z - m)) * (float)(1.0 / den) : __fdividef(1.0f, 1.0f + expf(-z));
+        wt = !live     ? 0.0f
+             : SOFTMAX ? (z == m ? 1.0f : expf(z - m)) * (float)(1.0 / den)
+                       : __fdividef(1.0f, 1.0f + expf(-z));
     if (lane < k) {
         a.idx[(size_t)t * k + lane] = mine;
         a.w[(size_t)t * k + lane] = wt * a.o.scale;
@@ -819,9 +824,12 @@ static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 // the chunks of the kept groups are merged to the lane's four best.
 //
 // SCORED: the values compared are sigmoid + bias.  Otherwise (no bias, groups by
-// their best expert) they are the logits, whose order is that of the scores:
-// logits that differ by 2^-30 or more, and neither saturate (z <= 24, sigmoid)
-// nor underflow (600 below 0 or the largest), differ as 64-bit scores.
+// their best expert) they are the logits, whose order is that of the scores.
+// Logits z + D and z differ as 64-bit scores where neither underflows (600 below
+// 0, or below the largest) and, softmax, D >= 2^-30; sigmoid, e^-z D > 2^-50 (1 +
+// e^-z lies on a grid of 2^-52): D >= 2^-30 up to z = 13, 2^-16 up to 20, and
+// beyond 13 values that the low bits tell apart differ by 2^-17 at least, at 20
+// e^-z D is then 2^-46.
 //
 // Values too close are compared again by exact logits, or as 64-bit sigmoids, one
 // per lane (0.6% of the tokens of 256 normal logits with biases).  What is left
@@ -865,6 +873,7 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
     uint32_t group_of = 0u;  // 4 bits per chunk
 #pragma unroll
     for (int i = 0; i < NCH; ++i) group_of |= (uint32_t)((r + 8 * i) * a.chunk_inv >> 16 & 15) << (4 * i);
+    // without a bias kRelErr has room for the low bits: (2 x 88 + 12 + 63) 2^-24 < 2^-16
     const float rel_err = !SCORED || a.bias ? kTagErr : kRelErr;
     float2* tops = reinterpret_cast<float2*>(wm.d) + (lane >> 3) * kQuadTops;
     uint8_t* place = reinterpret_cast<uint8_t*>(wm.first) + (lane >> 3) * 16;  // lane of the s-th best

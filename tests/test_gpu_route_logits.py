@@ -592,7 +592,7 @@ def test_batch_masks_infinities_and_nan(score):
             assert moe.moe_get_last_error() == 6
 
 
-@pytest.mark.parametrize("T", [8, 9, 31, 32, 33, 64, 65, 97, 127, 128, 129])
+@pytest.mark.parametrize("T", [8, 9, 31, 32, 33, 64, 65, 97, 127, 128, 129, 131, 193, 255, 256, 257])
 def test_small_batches_at_each_form(T):
     for E, k, o, with_bias in ((256, 8, OPTS["groups2"], True), (64, 6, OPTS["softmax_as_scored"], False),
                                (60, 5, OPTS["sigmoid"], True), (96, 8, ot.Opts(score="softmax", groups=6, top_groups=3), False),
