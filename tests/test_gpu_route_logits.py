@@ -618,3 +618,46 @@ def test_rows_of_equal_values(T):
             check_route(z, bias, k, o)
             check_route(z, None, k, o)
     check_status()
+
+
+def test_graphs_replayed_on_two_streams_at_once():
+    """Gate logits, routing and its gradient of several sizes, one graph per size, replayed in turn on two streams."""
+    o = OPTS["groups2"]
+    co, runs = c_opts(o), []
+    for i, (T, d, E, k) in enumerate(((5, 512, 256, 8), (40, 256, 64, 6), (100, 128, 60, 4), (600, 512, 160, 6), (3000, 64, 256, 8))):
+        g = torch.Generator(device=DEV).manual_seed(50 + i)
+        x = (torch.round(torch.randn((T, d), generator=g, device=DEV) * 16) / 16).to(torch.bfloat16)
+        wg = (torch.round(torch.randn((E, d), generator=g, device=DEV) * 25) / 1024).to(torch.bfloat16)
+        r = dict(x=x, wg=wg, bias=make(T, E, 60 + i)[1], z=torch.empty((T, E), device=DEV),
+                 idx=torch.empty((T, k), dtype=torch.int32, device=DEV), w=torch.empty((T, k), device=DEV),
+                 counts=torch.empty(E, dtype=torch.int32, device=DEV), dw=torch.randn((T, k), generator=g, device=DEV),
+                 dz=torch.empty((T, E), device=DEV), stream=torch.cuda.Stream(), graph=torch.cuda.CUDAGraph())
+        sh = shape(T, E, k, d)
+
+        def calls(r=r, sh=sh):
+            moe.moe_gate_logits(r["x"], r["wg"], sh, r["z"])
+            moe.moe_route_logits(r["z"], r["bias"], sh, co, r["idx"], r["w"], r["counts"])
+            moe.moe_route_logits_backward(r["z"], r["idx"], r["dw"], None, sh, co, r["dz"])
+        calls()
+        torch.cuda.synchronize()
+        r["want"] = [r[n].clone() for n in ("z", "idx", "w", "counts", "dz")]
+        with torch.cuda.graph(r["graph"], stream=r["stream"]):
+            calls()
+        runs.append(r)
+    for r in runs:
+        for n in ("z", "w", "dz"):
+            r[n].fill_(float("nan"))
+        r["idx"].fill_(-7)
+        r["counts"].fill_(-7)
+    torch.cuda.synchronize()
+    two = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i, r in enumerate(runs):
+            with torch.cuda.stream(two[i % 2]):
+                r["graph"].replay()
+    torch.cuda.synchronize()
+    for r in runs:
+        for n, want in zip(("z", "idx", "w", "counts", "dz"), r["want"]):
+            assert torch.equal(r[n], want), n
+        check_route(r["z"], r["bias"], r["idx"].shape[1], o, tuple(r[n].cpu().numpy() for n in ("idx", "w", "counts")))
+    check_status()
