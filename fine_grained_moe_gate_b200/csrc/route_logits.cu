@@ -1090,8 +1090,9 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
             }
         }
         best = fmaxf(best, kMasked);
-        // every round one lane's (the last may find no expert left)
-        again |= sum8(taken) != k + (best > kLow);
+        // every round one lane's (the last may find no expert left).  Equal values of two lanes leave a later round
+        // empty, and the sum may come out right all the same where no more than k experts stand.
+        again |= sum8(taken) != k + (best > kLow) || (r < k && !(mine > kLow));
         float next = __shfl_down_sync(kFull, mine, 1);
         if (r == k - 1) next = best;
         if (!SCORED) {

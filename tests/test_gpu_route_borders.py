@@ -1,0 +1,85 @@
+"""GPU parity of moe_route_logits at the borders of its 32-bit choice: rows with
+no more experts to choose from than are chosen, sums that cancel, scores whose
+sum carries the error.  Indices and counts equal oracle/training.py's (float64);
+weights as in test_gpu_route_logits.py: (32 + 2D) u, u = 2^-24, D the spread of
+a softmax row's logits.
+"""
+import numpy as np
+import pytest
+import torch
+
+import fine_grained_moe_gate_b200 as moe
+from oracle import training as ot
+
+from gpu_harness import DEV, check_status
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TINY = 2.0 ** -120
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    moe.moe_get_last_error()
+    yield
+
+
+def run_route(z, bias, k, o):
+    T, E = z.shape
+    idx = torch.full((T, k), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, k), float("nan"), device=DEV)
+    counts = torch.full((E,), -7, dtype=torch.int32, device=DEV)
+    opts = moe.route_opts(o.score, o.groups, o.top_groups, o.group_top, o.renormalize, o.scale)
+    moe.moe_route_logits(z, bias, moe.MoEShape(T, 64, E, k, 128, 0, 128, moe.MOE_BF16), opts, idx, w, counts)
+    torch.cuda.synchronize()
+    return idx.cpu().numpy(), w.cpu().numpy(), counts.cpu().numpy()
+
+
+def check_route(z, bias, k, o):
+    idx, w, counts = run_route(z, bias, k, o)
+    zn = z.cpu().numpy()
+    ri, rw, rc, short = ot.route(zn, None if bias is None else bias.cpu().numpy(), k, o)
+    wrong = np.flatnonzero((idx != ri).any(axis=1))
+    assert len(wrong) == 0, (len(wrong), wrong[:3], idx[wrong[:3]], ri[wrong[:3]])
+    assert (counts == rc).all()
+    spread = 0.0
+    if o.score == "softmax":
+        f = np.where(np.isfinite(zn), zn, np.nan)
+        spread = (np.nanmax(f, axis=1) - np.nanmin(f, axis=1))[:, None]
+    assert (np.abs(w - rw) <= (32 + 2 * spread) * U * np.abs(rw) + TINY * abs(o.scale)).all()
+    return short
+
+
+@pytest.mark.parametrize("T", [3, 9, 40, 131, 600])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_exactly_k_experts_with_equal_values(T, score):
+    """As many experts as are chosen, equal values among them (in several lanes of a token at once): all experts, those
+    that a mask leaves, those of the kept groups."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    for E, k in ((8, 8), (5, 5), (7, 7), (2, 2), (1, 1), (4, 4)):
+        for z in (torch.zeros((T, E), device=DEV), torch.full((T, E), -3.0, device=DEV),
+                  torch.randint(-1, 2, (T, E), generator=g, device=DEV).float()):
+            for bias in (None, torch.full((E,), 0.25, device=DEV)):
+                assert not check_route(z, bias, k, ot.Opts(score=score)).any()
+    # masked but for k: experts in one lane, in lanes next to each other, in all lanes
+    for E, k, left in ((64, 8, range(0, 32, 4)), (64, 8, [0, 1, 2, 3, 32, 33, 34, 35]), (256, 8, [0, 5, 33, 64, 97, 130, 200, 255]),
+                       (60, 6, [3, 7, 11, 35, 39, 43]), (256, 8, [0, 1, 2, 3, 32, 33, 34, 35])):
+        z = torch.full((T, E), float("-inf"), device=DEV)
+        z[:, list(left)] = torch.randint(0, 2, (T, k), generator=g, device=DEV).float()
+        z[::2, list(left)] = 0.0
+        for bias in (None, torch.full((E,), -0.5, device=DEV)):
+            for renorm in (True, False):
+                assert not check_route(z, bias, k, ot.Opts(score=score, renormalize=renorm)).any()
+    # kept groups of k experts in all
+    for groups, per, top, gtop, k in ((8, 8, 1, 1, 8), (8, 8, 1, 2, 8), (8, 4, 2, 2, 8), (6, 3, 2, 1, 6), (4, 1, 3, 1, 3),
+                                      (8, 32, 1, 2, 8)):
+        z = torch.randint(-1, 1, (T, groups * per), generator=g, device=DEV).float()
+        z[::3] = 0.0
+        if per > k:  # of the kept group, all but k are masked
+            z.view(T, groups, per)[:, :, k:] = float("-inf")
+        for bias in (None, torch.full((groups * per,), 0.125, device=DEV)):
+            o = ot.Opts(score=score, groups=groups, top_groups=top, group_top=gtop)
+            assert not check_route(z, bias, k, o).any()
+    check_status()
