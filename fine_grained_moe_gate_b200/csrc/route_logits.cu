@@ -251,7 +251,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // largest score (x e^-x <= 0.37), 2^-20.3 each.  Without a bias values are
 // compared relatively (the bound counts for both), with one absolutely, plus
 // the rounding of v and its low bits, 16u (|v_a| + |v_b|).  A group's value
-// sums two.  1e-37 covers what is below the normal range.
+// sums two: see group_err.  1e-37 covers what is below the normal range.
 constexpr float kRelErr = 0x1p-16f, kAbsErr = 0x1p-19f, kSumErr = 0x1p-20f;
 constexpr float kLog2e = 1.4426950408889634f, kFltMax = 3.4028234664e38f;
 // A masked value, and the bound below which a value is one.  Finite biases are
@@ -330,6 +330,15 @@ __device__ __forceinline__ void best2(const float (&v)[VPT], float& x1, float& x
 __device__ __forceinline__ float cut_of(float best, float abs_err, float rel_err) {
     return fmaxf(best - (abs_err + 2.0f * rel_err * fabsf(best) + 1e-37f), kLow);
 }
+
+// How far a group's 32-bit value may be off: the errors of its one or two
+// members and the sum's rounding.  They follow the members' sizes; the sum may
+// be far smaller, with biases of both signs, so each group is held to its own.
+__device__ __forceinline__ float group_err(float x1, float x2, float abs_err, float rel_err) {
+    return 1.5f * abs_err + 2.0f * rel_err * (fabsf(x1) + fabsf(x2)) + 1e-37f;
+}
+// The least that a group may be worth (infinite sums of two forced experts: nothing is sure).
+__device__ __forceinline__ float least_value(float gv, float off) { return gv <= kFltMax ? gv - off : kMasked; }
 
 // The general way to the k + 1 best: all values of the kept groups (bit g LG
 // of kept) from cut up, compacted and ranked by counting.  Returns whether two
@@ -504,8 +513,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
                     x2 = fmaxf(fminf(x1, y1), fmaxf(x2, y2));
                     x1 = fmaxf(x1, y1);
                 }
-                float gv = a.o.group_top == 2 && x2 > kLow ? x1 + x2 : x1;
+                const bool two = a.o.group_top == 2 && x2 > kLow;
+                float gv = two ? x1 + x2 : x1;
                 if (!real) gv = kMasked;
+                const float off = group_err(x1, two ? x2 : 0.0f, abs_err, rel_err);
                 // a group's lanes share the comparison with the others
                 int ahead = 0;
                 for (int i = 0; i < a.o.groups; i += LG) {
@@ -515,13 +526,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
                 for (int o = 1; o < LG; o <<= 1) ahead += __shfl_xor_sync(kFull, ahead, o);
                 const bool keep = ahead < a.o.top_groups && gv > kLow;
                 kept = __ballot_sync(kFull, keep) & a.leaders;
-                // the last kept group against the best of the others
-                const float lo = -warp_max(keep ? -gv : kMasked), hi = warp_max(keep ? kMasked : gv);
-                const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
-                if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err))) {
+                // the least that a kept group may be worth against the most that another may
+                const float lo = -warp_max(keep ? -least_value(gv, off) : kMasked), hi = warp_max(keep ? kMasked : gv + off);
+                if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo > hi))) {
                     if (in_lanes) put();
-                    const float nth = a.o.group_top == 2 && x2 > kLow ? x2 : x1;
-                    kept = kept_groups64(a, row, all, cut_of(nth, abs_err, rel_err), lane);
+                    kept = kept_groups64(a, row, all, cut_of(two ? x2 : x1, abs_err, rel_err), lane);
                 }
                 if (a.direct) {
                     best4<VPT>(v, x, fifth);
@@ -987,15 +996,15 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
             const bool two = SCORED && a.o.group_top == 2 && x2 > kLow;
             float gv = two ? x1 + x2 : x1;
             if (!real) gv = kMasked;
+            const float off = group_err(x1, two ? x2 : 0.0f, abs_err, rel_err);
             int ahead = 0;
 #pragma unroll
             for (int o = 1; o < 8; ++o) ahead += __shfl_sync(kFull, gv, first_lane | ((r + o) & 7)) > gv;
             bool keep = ahead < a.o.top_groups && gv > kLow;
             kept = __ballot_sync(kFull, keep) >> first_lane & 0xffu;
-            // the last kept group against the best of the others
-            const float lo = -max8(keep ? -gv : kMasked), hi = max8(keep ? kMasked : gv);
-            const float err = 3.0f * abs_err + 2.0f * rel_err * (fabsf(lo) + fabsf(hi)) + 1e-37f;
-            const bool unsure = __popc(kept) > a.o.top_groups || (hi > kLow && !(lo - hi > err));
+            // the least that a kept group may be worth against the most that another may
+            const float lo = -max8(keep ? -least_value(gv, off) : kMasked), hi = max8(keep ? kMasked : gv + off);
+            const bool unsure = __popc(kept) > a.o.top_groups || (hi > kLow && !(lo > hi));
             const float least = SOFTMAX && !SCORED ? max8(gv) + kUnderflow : kUnderflow;  // a shuffle: by every lane
             if (!SCORED) again |= hi > kLow && (lo < least || (!SOFTMAX && hi > kSaturated));
             if (__any_sync(kFull, unsure)) {

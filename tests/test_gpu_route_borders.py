@@ -83,3 +83,42 @@ def test_exactly_k_experts_with_equal_values(T, score):
             o = ot.Opts(score=score, groups=groups, top_groups=top, group_top=gtop)
             assert not check_route(z, bias, k, o).any()
     check_status()
+
+
+@pytest.mark.parametrize("big", [0.5, 16.0, 1000.0])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_group_values_whose_summands_cancel(score, big):
+    """Biases of both signs, one positive in a group: the two best values of every group are about +big and -big, and
+    their sums, a few hundredths, lie closer to each other than the summands' 32-bit error."""
+    for groups, per, top, k, T in ((8, 32, 4, 8, 2000), (8, 2, 3, 6, 4000), (8, 8, 3, 12, 3000), (16, 8, 5, 8, 3000)):
+        E = groups * per
+        g = torch.Generator(device=DEV).manual_seed(E + k)
+        z = torch.randn((T, E), generator=g, device=DEV) * (0.002 if score == "sigmoid" else 0.05)
+        bias = torch.full((groups, per), -big, device=DEV)
+        bias[torch.arange(groups), torch.randint(0, per, (groups,), generator=g, device=DEV)] = big
+        bias = bias.view(-1)
+        o = ot.Opts(score=score, groups=groups, top_groups=top, group_top=2)
+        check_route(z, bias, k, o)
+        for t in range(0, 160, 8):  # the form of small batches
+            check_route(z[t:t + 8].contiguous(), bias, k, o)
+        # unequal summands: one group's members far from zero, another's near it
+        near = bias.clone()
+        near.view(groups, per)[::2] *= 2.0 ** -10
+        check_route(z, near, k, o)
+    check_status()
+
+
+def test_group_values_past_the_largest_number():
+    """Two forced experts in a group: their 32-bit sum is infinite, the 64-bit one is not."""
+    big = torch.finfo(torch.float32).max
+    g = torch.Generator(device=DEV).manual_seed(3)
+    z = torch.randn((300, 64), generator=g, device=DEV)
+    bias = torch.zeros(64, device=DEV)
+    for place, value in ((0, big), (1, big), (8, big), (9, big * 0.5), (16, big), (24, big * 0.6), (25, big * 0.6),
+                         (32, float("inf")), (40, -big)):
+        bias[place] = value
+    for score in ("sigmoid", "softmax"):
+        for top in (1, 2, 3, 4, 5):
+            for rows in (z, z[:8].contiguous()):
+                check_route(rows, bias, 6, ot.Opts(score=score, groups=8, top_groups=top, group_top=2))
+    check_status()
