@@ -251,12 +251,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // largest score (x e^-x <= 0.37), 2^-20.3 each.  Without a bias values are
 // compared relatively (the bound counts for both), with one absolutely, plus
 // the rounding of v and its low bits, 16u (|v_a| + |v_b|).  A group's value
-// sums two: see group_err.  1e-37 covers what is below the normal range.
+// sums two: see group_span.  1e-37 covers what is below the normal range.
 constexpr float kRelErr = 0x1p-16f, kAbsErr = 0x1p-19f, kSumErr = 0x1p-20f;
 constexpr float kLog2e = 1.4426950408889634f, kFltMax = 3.4028234664e38f;
 // A masked value, and the bound below which a value is one.  Finite biases are
-// held above it (those beyond -1e37 tie in 32 bits and are compared in 64).
-constexpr float kMasked = -kFltMax, kLow = -1e38f;
+// held above it (those beyond kLeastBias tie in 32 bits and are compared in 64).
+constexpr float kMasked = -kFltMax, kLow = -1e38f, kLeastBias = -1e37f;
 
 // v with its low bits (three, or those of MASK) replaced by j.
 template <uint32_t MASK = 7u>
@@ -331,14 +331,22 @@ __device__ __forceinline__ float cut_of(float best, float abs_err, float rel_err
     return fmaxf(best - (abs_err + 2.0f * rel_err * fabsf(best) + 1e-37f), kLow);
 }
 
-// How far a group's 32-bit value may be off: the errors of its one or two
-// members and the sum's rounding.  They follow the members' sizes; the sum may
-// be far smaller, with biases of both signs, so each group is held to its own.
-__device__ __forceinline__ float group_err(float x1, float x2, float abs_err, float rel_err) {
-    return 1.5f * abs_err + 2.0f * rel_err * (fabsf(x1) + fabsf(x2)) + 1e-37f;
+// What a group may be worth at least and at most, from its best member x1, its
+// other one x2 (two) and their 32-bit value gv.  The error is that of the members
+// and of the sum's rounding; it follows the members' sizes.  The sum may be far
+// smaller, with biases of both signs, so each group is held to its own.  Members
+// held above the lowest biases (kLeastBias) may be worth any less, those held at
+// the largest number (bias +inf) any more; a sum that is infinite says nothing.
+struct Span {
+    float least, most;
+};
+__device__ __forceinline__ Span group_span(float gv, float x1, float x2, bool two, float abs_err, float rel_err) {
+    const float off = 1.5f * abs_err + 2.0f * rel_err * (fabsf(x1) + (two ? fabsf(x2) : 0.0f)) + 1e-37f;
+    Span s;
+    s.least = gv <= kFltMax && (two ? x2 : x1) > 0.9f * kLeastBias ? gv - off : kMasked;
+    s.most = x1 < 3.4e38f ? gv + off : kFltMax;
+    return s;
 }
-// The least that a group may be worth (infinite sums of two forced experts: nothing is sure).
-__device__ __forceinline__ float least_value(float gv, float off) { return gv <= kFltMax ? gv - off : kMasked; }
 
 // The general way to the k + 1 best: all values of the kept groups (bit g LG
 // of kept) from cut up, compacted and ranked by counting.  Returns whether two
@@ -401,7 +409,7 @@ __device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&
             report(a.status, kStDeviceCheck);
         }
         odd |= fabsf(b[j]) > kFltMax;
-        if (b[j] != neg_inf()) b[j] = fmaxf(fminf(b[j], kFltMax), -1e37f);
+        if (b[j] != neg_inf()) b[j] = fmaxf(fminf(b[j], kFltMax), kLeastBias);
         if (e0 + j >= E) b[j] = kMasked;
     }
     odd = __any_sync(kFull, odd);
@@ -516,7 +524,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
                 const bool two = a.o.group_top == 2 && x2 > kLow;
                 float gv = two ? x1 + x2 : x1;
                 if (!real) gv = kMasked;
-                const float off = group_err(x1, two ? x2 : 0.0f, abs_err, rel_err);
+                const Span span = group_span(gv, x1, x2, two, abs_err, rel_err);
                 // a group's lanes share the comparison with the others
                 int ahead = 0;
                 for (int i = 0; i < a.o.groups; i += LG) {
@@ -527,7 +535,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
                 const bool keep = ahead < a.o.top_groups && gv > kLow;
                 kept = __ballot_sync(kFull, keep) & a.leaders;
                 // the least that a kept group may be worth against the most that another may
-                const float lo = -warp_max(keep ? -least_value(gv, off) : kMasked), hi = warp_max(keep ? kMasked : gv + off);
+                const float lo = -warp_max(keep ? -span.least : kMasked), hi = warp_max(keep ? kMasked : span.most);
                 if (__popc(kept) > a.o.top_groups || (hi > kLow && !(lo > hi))) {
                     if (in_lanes) put();
                     kept = kept_groups64(a, row, all, cut_of(two ? x2 : x1, abs_err, rel_err), lane);
@@ -871,7 +879,7 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
             if (c < chunks && off < a.run) {
                 b = a.bias ? a.bias[g * a.run + off] : 0.0f;
                 if (b != b) report(a.status, kStDeviceCheck);
-                b = b > neg_inf() ? fmaxf(fminf(b, kFltMax), -1e37f) : kMasked;
+                b = b > neg_inf() ? fmaxf(fminf(b, kFltMax), kLeastBias) : kMasked;
             }
             reinterpret_cast<float*>(bias)[i] = b;
         }
@@ -996,14 +1004,14 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
             const bool two = SCORED && a.o.group_top == 2 && x2 > kLow;
             float gv = two ? x1 + x2 : x1;
             if (!real) gv = kMasked;
-            const float off = group_err(x1, two ? x2 : 0.0f, abs_err, rel_err);
+            const Span span = group_span(gv, x1, x2, two, abs_err, rel_err);
             int ahead = 0;
 #pragma unroll
             for (int o = 1; o < 8; ++o) ahead += __shfl_sync(kFull, gv, first_lane | ((r + o) & 7)) > gv;
             bool keep = ahead < a.o.top_groups && gv > kLow;
             kept = __ballot_sync(kFull, keep) >> first_lane & 0xffu;
             // the least that a kept group may be worth against the most that another may
-            const float lo = -max8(keep ? -least_value(gv, off) : kMasked), hi = max8(keep ? kMasked : gv + off);
+            const float lo = -max8(keep ? -span.least : kMasked), hi = max8(keep ? kMasked : span.most);
             const bool unsure = __popc(kept) > a.o.top_groups || (hi > kLow && !(lo > hi));
             const float least = SOFTMAX && !SCORED ? max8(gv) + kUnderflow : kUnderflow;  // a shuffle: by every lane
             if (!SCORED) again |= hi > kLow && (lo < least || (!SOFTMAX && hi > kSaturated));

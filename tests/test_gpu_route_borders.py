@@ -122,3 +122,24 @@ def test_group_values_past_the_largest_number():
             for rows in (z, z[:8].contiguous()):
                 check_route(rows, bias, 6, ot.Opts(score=score, groups=8, top_groups=top, group_top=2))
     check_status()
+
+
+def test_group_values_with_forced_and_masked_members():
+    """Biases of the type's largest and lowest value in one group: in 64 bits they cancel, or make the group the last."""
+    big = torch.finfo(torch.float32).max
+    g = torch.Generator(device=DEV).manual_seed(4)
+    z = torch.randn((300, 32), generator=g, device=DEV)
+    for pairs in ([(big, -big), (5e36, -big), (0.0, -2e37), (0.0, 0.0)],
+                  [(float("inf"), -1e36), (big, 0.0), (big, big), (1e30, -big)],
+                  [(-big, -big), (-2e37, -2e37), (-0.5e37, -0.5e37), (2e37, -big)]):
+        bias = torch.full((8, 4), -big, device=DEV)
+        for i, pair in enumerate(pairs):  # groups 2 i and 2 i + 1
+            bias[2 * i, 1:3] = torch.tensor(pair)
+            bias[2 * i + 1, :2] = torch.tensor(pair)
+        bias = bias.view(-1)
+        for score in ("sigmoid", "softmax"):
+            for top in range(2, 8):
+                for gtop in (1, 2):
+                    for rows in (z, z[:8].contiguous()):
+                        check_route(rows, bias, 4, ot.Opts(score=score, groups=8, top_groups=top, group_top=gtop))
+    check_status()
