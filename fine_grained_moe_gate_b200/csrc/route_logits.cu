@@ -243,16 +243,21 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // Where a lane would need its fifth, or two values are equal, all values from the
 // threshold found up are compacted and ranked by counting instead.
 //
-// Error bounds, u = 2^-24.  e = 2^(x log2 e): the product's rounding |x| u,
-// the hardware's 2 ulp (4u), 1 + e and its reciprocal (3u), for softmax the
-// rounding of z - m (|z - m| u) and the product with 1 / sum, whose own error
-// is a common factor.  Relative to s: at most (2 |x| + 12) u <= 2^-16.3 (the
-// exponential is 0 from |x| = 88 on).  Absolute: (2 * 0.37 + 12) u times the
-// largest score (x e^-x <= 0.37), 2^-20.3 each.  Without a bias values are
-// compared relatively (the bound counts for both), with one absolutely, plus
-// the rounding of v and its low bits, 16u (|v_a| + |v_b|).  A group's value
-// sums two: see group_span.  1e-37 covers what is below the normal range.
-constexpr float kRelErr = 0x1p-16f, kAbsErr = 0x1p-19f, kSumErr = 0x1p-20f;
+// Error bounds, u = 2^-24.  e = 2^(x log2 e): the product's rounding and the
+// constant's, 1.3 |x| u, the hardware's 2 ulp (4u), 1 + e and its reciprocal
+// (3u), for softmax the rounding of z - m (|z - m| u) and the product with
+// 1 / sum.  Relative to s: at most (2.3 |x| + 12) u <= 2^-16.2 (the exponential
+// is 0 from |x| = 88 on), the error of 1 / sum left out: without a bias it is a
+// factor of every value compared.  Absolute: (2.3 * 0.37 + 4 + 3) u <= 8u times the
+// largest score (x e^-x <= 0.37) each, 16u for two; for softmax scores with a bias
+// the difference of two also carries the error of 1 / sum: the terms' own, (2.3 |x|
+// + 4) u with |x| averaged over the scores (at most 3.4: 255 terms of e^-4.3 beside
+// the largest), 7 additions in a lane, 5 across lanes and the reciprocal's 2u, 26u.
+// Without a bias values are compared relatively (the bound counts for both), with
+// one absolutely, plus the rounding of v and its low bits, 16u (|v_a| + |v_b|).  A
+// group's value sums two: see group_span.  1e-37 covers what is below the normal
+// range.
+constexpr float kRelErr = 0x1p-16f, kAbsErr = 0x1p-19f, kAbsErrSoftmax = 0x1p-18f, kSumErr = 0x1p-20f;
 constexpr float kLog2e = 1.4426950408889634f, kFltMax = 3.4028234664e38f;
 // A masked value, and the bound below which a value is one.  Finite biases are
 // held above it (those beyond kLeastBias tie in 32 bits and are compared in 64).
@@ -482,7 +487,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
     #pragma unroll
                 for (int j = 0; j < VPT; ++j)
                     if ((masked >> j) & 1u) v[j] = kMasked;
-            const float abs_err = a.bias ? top * kAbsErr : 0.0f, rel_err = a.bias ? kSumErr : kRelErr;
+            const float abs_err = a.bias ? top * (SOFTMAX ? kAbsErrSoftmax : kAbsErr) : 0.0f, rel_err = a.bias ? kSumErr : kRelErr;
 
             float x[4] = {kMasked, kMasked, kMasked, kMasked}, fifth = kMasked;
             unsigned kept = a.leaders;

@@ -143,3 +143,22 @@ def test_group_values_with_forced_and_masked_members():
                     for rows in (z, z[:8].contiguous()):
                         check_route(rows, bias, 4, ot.Opts(score=score, groups=8, top_groups=top, group_top=gtop))
     check_status()
+
+
+@pytest.mark.parametrize("depth", [0.5, 2.0, 3.0, 4.3, 5.5])
+def test_softmax_with_a_bias_near_the_error_of_its_sum(depth):
+    """One large logit beside many equal ones: the error of 1 / sum then weighs most.  Biases set the large score against
+    the others' to within -80 .. 80 units of 2^-24, of which 35 may be the 32-bit values' error."""
+    E, k = 256, 1
+    g = torch.Generator(device=DEV).manual_seed(int(depth * 10))
+    for step in range(-80, 81, 4):
+        T = 200
+        z = torch.full((T, E), -depth, device=DEV)
+        z += torch.randn((T, 1), generator=g, device=DEV) + torch.randn((T, E), generator=g, device=DEV) * 1e-7
+        z[:, 17] += depth
+        s = torch.softmax(z[0].double(), dim=0)
+        bias = torch.zeros(E, device=DEV)
+        bias[17] = -(s[17] - s[40] + step * 2.0 ** -24 * s[17]).float()
+        check_route(z, bias, k, ot.Opts(score="softmax"))
+        check_route(z[:8].contiguous(), bias, k, ot.Opts(score="softmax", groups=2, top_groups=1, group_top=2))
+    check_status()
