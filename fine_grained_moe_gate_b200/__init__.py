@@ -244,18 +244,21 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-_dtypes: dict = {}
-_functions: dict = {}
+_tables: tuple = ()
 
 
 def _prepare():
+    """The dtypes by name and the entry points, as _call looks them up: one assignment, so that another thread finds
+    both or neither."""
+    global _tables
     import torch
-    _dtypes.update((n, getattr(torch, n)) for n in ("float32", "bfloat16", "int32", "uint8"))
-    _functions.update((n, getattr(lib(), n)) for n in EXPORTS)
+    _tables = ({n: getattr(torch, n) for n in ("float32", "bfloat16", "int32", "uint8")},
+               {n: getattr(lib(), n) for n in EXPORTS})
+    return _tables
 
 
-def _refuse(name, what, t, dtype, n, dev):
-    if t.dtype is not _dtypes[dtype]:
+def _refuse(name, what, t, dtype, n):
+    if t.dtype is not _tables[0][dtype]:
         raise MoEError(1, f"{name}: {what} must be {dtype}, got {t.dtype}")
     if t.numel() < n or not t.is_contiguous():
         raise MoEError(1, f"{name}: {what} must be contiguous with at least {n} elements, got {tuple(t.shape)}, strides "
@@ -270,21 +273,20 @@ def _call(name, stream, *args):
     the device of the others.  None and raw pointers go through as they are.
     The call runs with the tensors' device current, on its current stream
     unless one is given."""
-    if not _dtypes:
-        _prepare()
+    dtypes, functions = _tables or _prepare()
     dev, out = -1, []
     for a in args:
         if type(a) is tuple:
             what, a, dtype, n = a
             if a is not None and type(a) is not int:
                 d = a.get_device()
-                if (d < 0 or dev != d and dev >= 0 or a.dtype is not _dtypes[dtype] or a.numel() < n
+                if (d < 0 or dev != d and dev >= 0 or a.dtype is not dtypes[dtype] or a.numel() < n
                         or not a.is_contiguous()):
-                    _refuse(name, what, a, dtype, n, dev)
+                    _refuse(name, what, a, dtype, n)
                 dev = d
                 a = a.data_ptr()
         out.append(a)
-    fn = _functions[name]
+    fn = functions[name]
     if dev < 0:
         status = fn(*out, _stream(stream))
     else:
