@@ -658,7 +658,6 @@ __device__ __forceinline__ void finish_counts(const RouteArgs& a, const int* his
         cluster_sync_all();  // no CTA leaves while its counts are read
     } else {
         __syncthreads();
-        grid_dependency_wait();  // the counters are clear
         for (int e = tid; e < E; e += WARPS * 32)
             if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
     }
@@ -673,10 +672,10 @@ __global__ void __launch_bounds__(WARPS * 32, SMALL ? 1 : 4)
     int* taken_tokens = hist + kMaxExperts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int E = a.E;
-    if (SMALL) grid_dependency_wait();
     for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
     if (tid == 0) *taken_tokens = WARPS;
     __syncthreads();
+    grid_dependency_wait();  // the logits and biases, and the cleared counters
 
     float b[VPT];
     bool odd;
@@ -876,7 +875,8 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
     int* hist = reinterpret_cast<int*>(bias + 8 * NCH);
     const int tid = threadIdx.x, lane = tid & 31, r = lane & 7, first_lane = lane & 24;
     const int E = a.E, k = a.k, chunks = a.chunks;
-    if (SMALL) grid_dependency_wait();
+    for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
+    grid_dependency_wait();  // the logits and biases, and the cleared counters
     if (SCORED)
         for (int i = tid; i < 8 * N; i += WARPS * 32) {
             const int c = i >> 2, g = c * a.chunk_inv >> 16, off = 4 * (c - g * a.run_chunks) + (i & 3);
@@ -888,7 +888,6 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
             }
             reinterpret_cast<float*>(bias)[i] = b;
         }
-    for (int e = tid; e < E; e += WARPS * 32) hist[e] = 0;
     __syncthreads();
 
     const bool vec = (a.run & 3) == 0, grouped = a.o.top_groups < a.o.groups;
@@ -1191,8 +1190,9 @@ __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuad
     finish_counts<WARPS, SMALL>(a, hist, tid);
 }
 
-// Clears the counters.  The routing kernel starts beside it, once everything
-// before both is complete, and waits for this kernel's end before it adds.
+// Clears the counters.  The routing kernel's CTAs take their places meanwhile;
+// they wait for this kernel's end, and with it for all before it, before they
+// read or add anything (reading beside it instead took the same time).
 __global__ void clear_counts_kernel(int32_t* counts, int E) {
     grid_dependency_wait();
     grid_launch_dependents();

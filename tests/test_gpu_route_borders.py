@@ -162,3 +162,47 @@ def test_softmax_with_a_bias_near_the_error_of_its_sum(depth):
         check_route(z, bias, k, ot.Opts(score="softmax"))
         check_route(z[:8].contiguous(), bias, k, ot.Opts(score="softmax", groups=2, top_groups=1, group_top=2))
     check_status()
+
+
+@pytest.mark.parametrize("T,d,E,k", [(130, 64, 64, 6), (700, 256, 160, 6), (2500, 64, 256, 8), (6000, 128, 256, 8), (3000, 64, 256, 12)])
+def test_each_replay_sees_its_own_inputs(T, d, E, k):
+    """Gate logits, routing and its gradient in one graph: replays on changing tokens and biases, one behind the other,
+    give what the same calls give with a synchronisation after each."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    sh = moe.MoEShape(T, d, E, k, 128, 0, 128, moe.MOE_BF16)
+    co = moe.route_opts(groups=4, top_groups=2, group_top=2)
+    n = 8
+    xs = torch.randn((n, T, d), generator=g, device=DEV).bfloat16()
+    bs = (torch.rand((n, E), generator=g, device=DEV) - 0.5) * 0.1
+    wg = (torch.randn((E, d), generator=g, device=DEV) * 0.05).bfloat16()
+    dw = torch.randn((T, k), generator=g, device=DEV)
+    x, bias, z, dz = xs[0].clone(), bs[0].clone(), torch.empty((T, E), device=DEV), torch.empty((T, E), device=DEV)
+    idx, w = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    counts = torch.empty(E, dtype=torch.int32, device=DEV)
+    steps = [lambda: moe.moe_gate_logits(x, wg, sh, z), lambda: moe.moe_route_logits(z, bias, sh, co, idx, w, counts),
+             lambda: moe.moe_route_logits_backward(z, idx, dw, None, sh, co, dz)]
+    out = (z, idx, w, counts, dz)
+    want = []
+    for i in range(n):
+        x.copy_(xs[i])
+        bias.copy_(bs[i])
+        for step in steps:
+            step()
+            torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for step in steps:
+            step()
+    for rounds in range(3):
+        got = []
+        for i in range(n):
+            x.copy_(xs[i])
+            bias.copy_(bs[i])
+            graph.replay()
+            got.append([t.clone() for t in out])
+        torch.cuda.synchronize()
+        for i in range(n):
+            for a, b in zip(got[i], want[i]):
+                assert torch.equal(a, b), (rounds, i)
+    check_status()
