@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32) swiglu_bwd_saved_kernel(const __g
                 da[j] = dh * g[j] * fmaf(as, s1, s);  // g s (1 + a (1 - s))
                 dg[j] = dh * as;
             }
-            if (q < 0)  // a row without an assignment: zeros, whatever it holds
+            if (q < 0)  // a row without an assignment: no gradient, whatever its codes and u hold (h is theirs alone)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) da[j] = dg[j] = 0.0f;
             __stcs(reinterpret_cast<uint4*>(dadg + c),

@@ -537,7 +537,9 @@ MOE_API moe_status moe_ffn_up_save(const void* x_perm, const int32_t* offsets, c
  * MOE_ROUTED: row r is assignment q = perm_tok[r], wt = topk_w[q], and dw[q]
  *   = sum_i u[r][i] (a s g)[i] (unrounded), the gradient of topk_w for u = dy
  *   W2;  perm_tok (moe_permute's) [T*k], topk_w [T*k], dw [T*k].  An entry of perm_tok outside
- *   [0, T*k) is reported (MOE_ERR_DEVICE_CHECK); its row gets zeros.
+ *   [0, T*k) is reported (MOE_ERR_DEVICE_CHECK): its row of dadg gets zeros and no dw is
+ *   written.  h does not depend on perm_tok: it is a s g of the row's codes, whatever those
+ *   hold (of rows that no expert took, which the forward leaves unwritten, nothing of meaning).
  * MOE_SHARED: wt = 1; perm_tok, topk_w and dw are ignored (may be NULL).
  * u [rows][n] fp32 (the gradient at h before the weight); dadg, h bf16. */
 MOE_API moe_status moe_swiglu_backward_saved(const moe_saved_acts* saved, moe_shape sh, int32_t set, const float* u,
