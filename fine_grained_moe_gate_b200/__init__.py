@@ -639,7 +639,8 @@ def moe_layer_backward_logits(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape, opts,
     a = _layer_args(x, w_gate, w1, w3, w2, ws1, ws3, ws2, shape)
     _call("moe_layer_backward_logits", stream, a["x"], a["w_gate"], a["w1"], a["w3"], a["w2"], a["ws1"], a["ws3"],
           a["ws2"], shape, opts,
-          _saved_ref("moe_layer_backward_logits", saved, shape, ("", "s") if shape.S > 0 else ("",), _device(x)), f("logits", logits, T * E), ("topk_idx", topk_idx, "int32", T * k),
+          _saved_ref("moe_layer_backward_logits", saved, shape, ("", "s") if shape.S > 0 else ("",), _device(x)),
+          f("logits", logits, T * E), ("topk_idx", topk_idx, "int32", T * k),
           f("topk_w", topk_w, T * k), ("counts", counts, "int32", E), f("dscores", dscores, T * E), f("dy", dy, T * d),
           float(alpha), int(seq_len), f("dx", dx, T * d), f("dw_gate", dw_gate, E * d), f("dw1", dw1, EId),
           f("dw3", dw3, EId), f("dw2", dw2, EId), f("dws1", dws1, SI * d), f("dws3", dws3, SI * d),

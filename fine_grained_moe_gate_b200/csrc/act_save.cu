@@ -8,11 +8,11 @@
 //   routed: dw[q] = sum_i u_i h_i  (h unrounded), wt = w[q], q = perm[r].
 //
 // HBM bound: per element 2 codes + 2/32 scale bytes and 4 of u in, 4 of dadg
-// and 2 of h out.  65536 rows of 2048: 242 us, 6.7 TB/s, above the rate of a
-// plain copy.  That takes four chunks of a row in flight per lane, streaming
-// loads and stores, 4 warps per CTA (8 warps: 246 us, two chunks: 252) and the
-// hardware's exponential (250 with expf; with it, plain loads and stores took
-// 5 us more, one chunk 15 more).
+// and 2 of h out, 1.62 GB for 65536 rows of 2048.  245 us in a short run, 254 to
+// 264 for calls on end (6.1 to 6.6 TB/s, the rate of a plain copy).  That takes
+// four chunks of a row in flight per lane, streaming loads and stores, 4 warps per
+// CTA and the hardware's exponential; against the same kernel in one run 8 warps
+// took 4 us more, two chunks 10, plain loads and stores 5, one chunk 15, expf 8.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

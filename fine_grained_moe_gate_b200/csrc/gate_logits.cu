@@ -8,11 +8,11 @@
 // fill too few SMs split K over the CTAs (or pairs) of a cluster, whose
 // partial sums meet in the fixed order 0..C-1 through distributed shared
 // memory, and the experts over chunks: a decoding step of 64 tokens (d = 7168,
-// 256 experts) is bound by what one SM can take in and by latency; 8 slices of
-// one chunk took 11.3 us, of 8 chunks 6.8.  Large batches are HBM bound: x is
-// read once (8192 x 7168: 117 MB, 18.2 us at the copy rate; the kernel takes
-// 27.5, the difference is its start, the exchange of the two K halves and the
-// store).
+// 256 experts) is bound by what one SM can take in and by latency: 6.4 us (8
+// slices of one chunk took 11.3, of 8 chunks 6.8 in the same run).  Large batches
+// are HBM bound: x is read once (8192 x 7168: 117 MB, 18.2 us at the copy rate; the
+// kernel takes 28.4, the difference is its start, the exchange of the two K halves
+// and the store; its 32 tiles of two K halves fill 128 of 148 SMs).
 #include "common.cuh"
 #include "kernels.h"
 #include "pdl.h"
@@ -348,7 +348,7 @@ cudaError_t launch_gate_logits_tc(const void* x, const void* wg, int T, int d, i
     // the least cost of what a CTA loads and of the partial sums it exchanges.
     // A byte of those weighs as 7 loaded (1536 tokens: 4 slices x 2 chunks 12.1
     // us, 8 x 1 16.0; 3000: 2 x 2 16.2, 4 x 1 17.9); whole sums, twice as long,
-    // have to gain 5% over two halves (8192 tokens: 27.5 us both).
+    // have to gain 5% over two halves (8192 tokens: the same time both).
     int split = 1, n_sub = n16 * 16;
     double least = 0.0;
     for (int s = pair ? 4 : 8; s >= 1; s >>= 1) {

@@ -208,6 +208,9 @@ __device__ __noinline__ int reorder64(const RouteArgs& a, const float* row, Warp
 // its SLOTS lanes (lanes without one: live false).  s = e^min(z,0) / (1 +
 // e^-|z|) (sigmoid) or e^z / const (softmax), with the largest exponent taken
 // out of the ratio, so that it stands where every score underflows.
+// __fdividef here and below: 2 ulp instead of half of one, a reciprocal and a
+// product.  Its divisors lie between 1 and 256, or are 1 + e^|z|, whose quotient it
+// flushes to 0 only below the normal range.
 template <int SLOTS>
 __device__ __forceinline__ float chosen_share(float z, bool live, bool softmax) {
     const float x = softmax ? z : fminf(z, 0.0f);
@@ -476,6 +479,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, WarpMem& wm, int
                 }
     #pragma unroll
                 for (int j = 0; j < VPT; ++j) part += v[j];
+                // also the factor of weights as scored: off by at most 26 units of 2^-24 (see kAbsErrSoftmax), once
+                // per weight
                 top = rcp_fast(fmaxf(warp_sum(part), 1e-30f));
     #pragma unroll
                 for (int j = 0; j < VPT; ++j) v[j] = tagged(fmaf(v[j], top, b[j]), j);
@@ -826,8 +831,8 @@ __device__ __forceinline__ T sum8(T v) {
 }
 
 // Warps per CTA and CTAs per SM of a batch: 80 registers for the 32 values of a lane, 64
-// for fewer (8192 x 256 sigmoid groups: 8.7 us, with 64 registers 9.3; 32768 x
-// 160 softmax groups: 12.1 us, with 80 13.4).  More and smaller CTAs add up
+// for fewer (side by side, inputs in L2: 8192 x 256 sigmoid groups 8.7 us, with 64
+// registers 9.3; 32768 x 160 softmax groups 12.1 us, with 80 13.4).  More and smaller CTAs add up
 // more counts (one atomic per expert and CTA).  A small batch: one cluster of as
 // many CTAs as it fills, one up to 32 tokens (the cluster's barrier and reads
 // cost 0.8 us; 4 warps per CTA 0.6 more at 32, 16 warps 0.2 to 1.5 at 64 to 128).
@@ -856,10 +861,12 @@ static_assert(4 * kQuadTops * sizeof(float2) <= offsetof(WarpMem, sorted), "");
 // per lane (0.6% of the tokens of 256 normal logits with biases).  What is left
 // (closer still, NaN, +inf, too few experts) is done by route_token64, 6 us.
 //
-// Issue bound (figures with the logits in L2): 32768 x 160 softmax tokens in
-// groups execute 250 instructions each and take 12.1 us (a warp per token 36;
-// the logits at the copy rate 3.3), 32768 x 256 sigmoid tokens in groups 19.8
-// (34.6; 5.2), 8192 x 256 8.8 (14.4; 1.3), of which about 3 are the two launches.
+// Bound by the chain of one quad's instructions, 1579 of 256 sigmoid experts in
+// groups, more than by issue slots (38% busy at 8192 tokens, 57% at 32768 x 160):
+// 8192 x 256 sigmoid tokens in groups take 8.7 to 10.5 us, of which about 3 are the
+// two launches, 32768 x 256 22, 32768 x 160 softmax tokens in groups, 250
+// instructions each, 12.5 to 13.8 (the logits at the copy rate: 1.3, 5.2, 3.3).  A
+// warp per token took 1.6 to 3 times as long.
 template <int NCH, bool SOFTMAX, bool SCORED, bool SMALL>
 __global__ void __launch_bounds__(quad_warps(NCH, SMALL) * 32, SMALL ? 1 : kQuadCtas)
     route_logits_quad_kernel(const __grid_constant__ RouteArgs a) {

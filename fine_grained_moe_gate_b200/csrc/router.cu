@@ -137,7 +137,10 @@ cudaError_t launch_router_simt(const void* x, const void* wg, const float* bias,
 // Gate logits of an fp32 layer: z = x W_gate^T, FFMA in k order.  A CTA takes
 // 32 tokens x 32 experts (small layers: many small tiles fill more SMs than
 // the router's 32 tokens x E), each of its 128 threads 2 x 4 of them; 32-wide
-// K chunks go through shared memory.
+// K chunks go through shared memory.  Bound by the latency of a chunk's loads and
+// barriers, 1 to 2 us with nothing in flight meanwhile: 17.5 us at d = 512 (64 x 64
+// as 512 x 256), 134 at 4096 x 2048 x 64, where FFMA alone would take 15 and the
+// library's product takes 62.  fp32 layers are the small ones.
 __global__ void __launch_bounds__(128) gate_logits_simt_kernel(const float* __restrict__ x,
                                                                const float* __restrict__ wg, int T, int d, int E,
                                                                float* __restrict__ z) {

@@ -550,6 +550,8 @@ MOE_API moe_status moe_swiglu_backward_saved(const moe_saved_acts* saved, moe_sh
  * moe_layer_forward_logits / moe_layer_backward_logits -- the layer and its
  * gradients with routing from logits, in any of its forms, and with or without
  * saved activations.
+ *   MOE_F32 and MOE_BF16 layers (MOE_ERR_UNSUPPORTED otherwise: an E4M3 layer
+ *   calls moe_gate_logits, moe_route_logits and the _fp8 calls one by one).
  *   forward: moe_gate_logits (into logits [T][E], kept for the backward),
  *     moe_route_logits, moe_permute, moe_ffn_up_save (saved != NULL; bf16
  *     layers) or moe_ffn_up, moe_ffn_down, moe_combine.  bias may be NULL.
